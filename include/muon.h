@@ -63,7 +63,11 @@ typedef enum muon_status_t {
                                     coordinate check failed, the access was skipped   */
 } muon_status_t;
 
-typedef enum muon_dtype_t { MUON_F32 = 0, MUON_BF16 = 1 } muon_dtype_t;
+typedef enum muon_dtype_t {
+  MUON_F32 = 0,
+  MUON_BF16 = 1,
+  MUON_E4M3 = 2 /* 8-bit codes; only as the output of muon_rmsnorm_forward */
+} muon_dtype_t;
 
 /* Update scale s(rows, cols) of the STORED parameter shape. */
 typedef enum muon_scale_rule_t {
@@ -347,6 +351,191 @@ muon_status_t muon_debug_inject_stall(int what);
  * launches and 4 KB per buffer.  Errors: bad_bytes NULL ->
  * MUON_ERR_INVALID_ARGUMENT. */
 muon_status_t muon_debug_guard_check(cudaStream_t stream, int64_t *bad_bytes);
+
+/* ======================================================================
+ * The mixture-of-experts block whose parameters the optimizer step trains
+ * (expert tensors are the [E,M,N] groups of [HP] section 6.3, gains are
+ * AdamW's): RMS norm with the residual's addition, routing, and the
+ * experts' products, each with its gradient.  None of them is on the pages;
+ * the formulas are given here.
+ *
+ * Conventions, besides those at the top of this file:
+ *   - Row strides are in elements and at least the row's width; a stride is
+ *     read only where there is more than one row.
+ *   - Outputs must not overlap inputs or each other (MUON_ERR_ALIAS) except
+ *     where an entry point allows it.
+ *   - 16-byte aligned pointers and strides of a multiple of 16 bytes are
+ *     fastest; any element-aligned pointer and any stride works.
+ * ====================================================================== */
+
+/* h = x + residual (x alone when residual is NULL), in fp32;
+ * y = gain * h / sqrt(mean(h^2) + eps) per row, from the unrounded h.
+ *   x, residual  f32 or bf16 [rows, cols], each with its own dtype
+ *   gain         f32 or bf16 [cols]; NULL: ones
+ *   h            f32 or bf16 output, NULL: not written.  It may be the same
+ *                tensor as residual or x (same pointer, dtype and stride).
+ *   y            f32, bf16 or MUON_E4M3 output
+ *   scales       MUON_E4M3 only: f32 [rows, ceil(cols / group)] output, dense.
+ *                Row piece p stands for code * scale, where
+ *                scale = max(largest |y| of the piece, 1e-12) / 448 and a code
+ *                is y * (448 / that largest magnitude) rounded to nearest even.
+ *   group        MUON_E4M3: columns per scale, 0 (the whole row) or 128;
+ *                otherwise 0
+ * cols in [1, 32768], else MUON_ERR_UNSUPPORTED.  rows 0 is a no-op. */
+typedef struct muon_rmsnorm_t {
+  int64_t rows, cols;
+  const void *x;
+  int64_t x_stride;
+  const void *residual;
+  int64_t residual_stride;
+  const void *gain;
+  void *h;
+  int64_t h_stride;
+  void *y;
+  int64_t y_stride;
+  float *scales;
+  int32_t x_dtype, residual_dtype, gain_dtype, h_dtype, y_dtype;
+  int32_t group;
+  float eps;
+} muon_rmsnorm_t;
+muon_status_t muon_rmsnorm_forward(const muon_rmsnorm_t *args, cudaStream_t stream);
+
+/* Gradient of muon_rmsnorm_forward.  With u = h / sqrt(mean(h^2) + eps):
+ *   dh    = (gain dy - u mean(gain dy u)) / sqrt(mean(h^2) + eps) + dres
+ *   dgain = sum over rows of dy u
+ *   dy, h  f32 or bf16 [rows, cols] (h as muon_rmsnorm_forward wrote it)
+ *   dres   f32 or bf16, the gradient that reaches h along the residual
+ *          stream; NULL: none
+ *   dh     f32 or bf16 output: the gradient of x and of residual.  It may be
+ *          the same tensor as dy or dres (same pointer, dtype and stride).
+ *   dgain  f32 [cols] output, NULL: not wanted.  Summed in a fixed order:
+ *          repeated calls give the same bits.  rows 0 writes zeros. */
+typedef struct muon_rmsnorm_grad_t {
+  int64_t rows, cols;
+  const void *dy;
+  int64_t dy_stride;
+  const void *h;
+  int64_t h_stride;
+  const void *gain;
+  const void *dres;
+  int64_t dres_stride;
+  void *dh;
+  int64_t dh_stride;
+  float *dgain;
+  int32_t dy_dtype, h_dtype, gain_dtype, dres_dtype, dh_dtype;
+  float eps;
+} muon_rmsnorm_grad_t;
+muon_status_t muon_rmsnorm_backward(const muon_rmsnorm_grad_t *args, cudaStream_t stream);
+
+/* Score of an expert from its logit. */
+typedef enum muon_route_score_t { MUON_ROUTE_SOFTMAX = 0, MUON_ROUTE_SIGMOID = 1 } muon_route_score_t;
+/* Rank of a group of experts among the groups. */
+typedef enum muon_group_score_t {
+  MUON_GROUP_MAX = 0, /* its best expert's key                                     */
+  MUON_GROUP_SUM2 = 1 /* the sum of its two largest score + bias (one: that one)   */
+} muon_group_score_t;
+
+/* Routing of tokens to experts.  Per token, from its logits l[experts]:
+ *   score_e = softmax(l)_e or 1 / (1 + exp(-l_e))
+ *   key_e   = score_e + bias_e, or l_e itself without a bias (both scores
+ *             grow with the logit)
+ *   the experts are cut into `groups` equal runs; the top_groups best ranked
+ *   stay, the others' experts are not chosen (top_groups == groups: no cut)
+ *   idx     = the top_k largest keys in falling order; ties, of experts and
+ *             of groups, go to the lowest index
+ *   weight  = scale * score_idx, with `renormalize` scale * score_idx / their
+ *             sum over the chosen (0 where that sum is 0)
+ * The bias acts on the choice only.  An expert whose logit is -inf is never
+ * chosen; NaN and +inf are read as -inf and set MUON_ERR_NONFINITE in the
+ * status word.  Slots that find no expert, and all slots of a token that
+ * `mask` leaves out, get idx -1 and weight 0. */
+typedef struct muon_route_config_t {
+  int32_t experts;     /* 1 .. 1024 */
+  int32_t top_k;       /* 1 .. 32, at most experts */
+  int32_t score;       /* muon_route_score_t */
+  int32_t groups;      /* 1 .. 64, divides experts */
+  int32_t top_groups;  /* 1 .. groups */
+  int32_t group_score; /* muon_group_score_t */
+  int32_t renormalize;
+  float scale;
+} muon_route_config_t;
+
+/* idx int32 and weights f32 [tokens, top_k] from logits (f32 or bf16, row
+ * stride `stride`), bias f32 [experts] or NULL, mask uint8 [tokens] (0: left
+ * out) or NULL; and, unless offsets is NULL, the plan of muon_route_plan.
+ * tokens * top_k < 2^31. */
+muon_status_t muon_route_forward(const muon_route_config_t *cfg, const void *logits, int32_t dtype,
+                                 int64_t stride, int64_t tokens, const float *bias,
+                                 const uint8_t *mask, int32_t *idx, float *weights,
+                                 int32_t *offsets, int32_t *src, int32_t *pos,
+                                 cudaStream_t stream);
+
+/* The rows of all (token, slot) pairs in expert order, and in token order
+ * within an expert (a stable counting sort; no order depends on timing):
+ *   offsets int32 [experts + 1]: expert e has rows [offsets[e], offsets[e+1])
+ *   src     int32 [tokens * top_k]: token * top_k + slot of a row; -1 for the
+ *           entries from offsets[experts] on
+ *   pos     int32 [tokens, top_k]: the row of a pair; -1 where idx is -1
+ * idx: int32 [tokens, top_k], each in [-1, experts) (others read as -1). */
+muon_status_t muon_route_plan(const int32_t *idx, int64_t tokens, int32_t top_k, int32_t experts,
+                              int32_t *offsets, int32_t *src, int32_t *pos, cudaStream_t stream);
+
+/* Gradient of the weights with respect to the logits (the choice is held
+ * fixed): dlogits [tokens, experts] in the logits' dtype, row stride
+ * dlogits_stride, from idx and dweights f32 [tokens, top_k].  Slots with
+ * idx -1 (or out of range) contribute nothing. */
+muon_status_t muon_route_backward(const muon_route_config_t *cfg, const void *logits, int32_t dtype,
+                                  int64_t stride, int64_t tokens, const int32_t *idx,
+                                  const float *dweights, void *dlogits, int64_t dlogits_stride,
+                                  cudaStream_t stream);
+
+/* The experts' products over a routing:
+ *   out[t] = sum_j weights[t,j] W_out[e] act(e, x_t),   e = idx[t,j],
+ *   act(e, x) = silu(W_gate[e] x) * (W_up[e] x),   silu(g) = g / (1 + exp(-g)),
+ * summed over the slots with pos[t,j] >= 0.
+ *   x      bf16 [tokens, hidden], row stride x_stride
+ *   w_in   bf16 [experts, 2 * inner, hidden]: rows [0, inner) of an expert
+ *          are W_gate, rows [inner, 2 inner) W_up (as [2 * experts, inner,
+ *          hidden] it is a muon_group_t of whole matrices)
+ *   w_out  bf16 [experts, hidden, inner]
+ *   weights, offsets, src, pos   as muon_route_forward wrote them
+ * Products accumulate in fp32; the activation and each slot's product are
+ * rounded to bf16 once (they are the next product's operand and the sum's
+ * terms).  out bf16 [tokens, hidden], row stride out_stride.
+ * gu: bf16 [tokens * top_k, 2 * inner] or NULL: the gate and up values of
+ * every row below offsets[experts], for muon_experts_backward (later rows
+ * are not written).
+ * tokens * top_k < 2^31, experts <= 1024, top_k <= 32, hidden and inner in
+ * [1, 65536].  The rows' intermediate values live in the library's workspace. */
+typedef struct muon_experts_t {
+  int64_t tokens, hidden, inner;
+  int32_t experts, top_k;
+  const void *x;
+  int64_t x_stride;
+  const void *w_in, *w_out;
+  const float *weights;
+  const int32_t *offsets, *src, *pos;
+} muon_experts_t;
+muon_status_t muon_experts_forward(const muon_experts_t *args, void *out, int64_t out_stride,
+                                   void *gu, cudaStream_t stream);
+
+/* Gradient of muon_experts_forward from dout bf16 [tokens, hidden] (row
+ * stride dout_stride) and the saved gu.  Per row r of token t, expert e, with
+ * (g, u) = gu[r], a = silu(g) u, da = W_out[e]^T dout_t, w its weight:
+ *   dweights[t,j] = <da, a>          (0 where pos is -1)
+ *   dgu     = w (da u silu'(g), da silu(g))
+ *   dx[t]   = sum_j W_in[e]^T dgu
+ *   dw_in[e]  = sum over the expert's rows of dgu x_t^T
+ *   dw_out[e] = sum over the expert's rows of dout_t (w a)^T
+ * dx bf16 [tokens, hidden] (row stride dx_stride); dw_in, dw_out shaped as
+ * the weights, dtype dw_dtype (f32 or bf16); dweights f32 [tokens, top_k].
+ * Any output may be NULL: not wanted.  Experts without rows get zero weight
+ * gradients.  dgu and w a are rounded to bf16 once, as products' operands.
+ * No sum's order depends on timing. */
+muon_status_t muon_experts_backward(const muon_experts_t *args, const void *dout,
+                                    int64_t dout_stride, const void *gu, void *dx,
+                                    int64_t dx_stride, void *dw_in, void *dw_out,
+                                    int32_t dw_dtype, float *dweights, cudaStream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char *muon_status_string(muon_status_t status);

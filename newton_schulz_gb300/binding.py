@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Iterable, Optional, Sequence
+from typing import Iterable, NamedTuple, Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmuon.so")
@@ -19,7 +19,9 @@ STATUS_NAMES = {
     3: "MUON_ERR_ALIAS", 4: "MUON_ERR_OUT_OF_MEMORY", 5: "MUON_ERR_CUDA",
     6: "MUON_ERR_TIMEOUT", 7: "MUON_ERR_NONFINITE", 8: "MUON_ERR_BOUNDS",
 }
-MUON_F32, MUON_BF16 = 0, 1
+MUON_F32, MUON_BF16, MUON_E4M3 = 0, 1, 2
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_SUM2 = 0, 1
 SCALE_SQRT_MAX1_R_OVER_C, SCALE_RMS_0P2_SQRT_MAXDIM, SCALE_ONE = 0, 1, 2
 NS_BF16, NS_TF32 = 0, 1
 PROFILE_KINDS = ("prep", "gram", "poly", "apply", "update", "fused_small", "adamw")
@@ -33,6 +35,9 @@ EXPORTED = (
     "muon_ns_path",
     "muon_ns_gram_restart",
     "muon_debug_build",
+    "muon_rmsnorm_forward", "muon_rmsnorm_backward",
+    "muon_route_forward", "muon_route_plan", "muon_route_backward",
+    "muon_experts_forward", "muon_experts_backward",
 )
 PATH_SMALL, PATH_XSPACE, PATH_GRAM_SPACE = 0, 1, 2
 INJECT_NONE, INJECT_GEMM, INJECT_SMALL = 0, 1, 2
@@ -73,6 +78,57 @@ class AdamwConfig(ctypes.Structure):
 class Unit(ctypes.Structure):
     _fields_ = [("cost", ctypes.c_double), ("bytes", ctypes.c_int64), ("elems", ctypes.c_int64),
                 ("layer", ctypes.c_int32)]
+
+
+class RmsNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("gain", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("h_stride", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64),
+                ("scales", ctypes.c_void_p),
+                ("x_dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("gain_dtype", ctypes.c_int32), ("h_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("group", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class RmsNormGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dy", ctypes.c_void_p), ("dy_stride", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("h_stride", ctypes.c_int64),
+                ("gain", ctypes.c_void_p),
+                ("dres", ctypes.c_void_p), ("dres_stride", ctypes.c_int64),
+                ("dh", ctypes.c_void_p), ("dh_stride", ctypes.c_int64),
+                ("dgain", ctypes.c_void_p),
+                ("dy_dtype", ctypes.c_int32), ("h_dtype", ctypes.c_int32),
+                ("gain_dtype", ctypes.c_int32), ("dres_dtype", ctypes.c_int32),
+                ("dh_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class RouteConfig(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class Experts(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inner", ctypes.c_int64),
+                ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("w_in", ctypes.c_void_p), ("w_out", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("src", ctypes.c_void_p), ("pos", ctypes.c_void_p)]
+
+
+class Route(NamedTuple):
+    """A routing as muon_route_forward returns it (int32, f32, int32 ...)."""
+    idx: object       # [tokens, top_k] expert of each slot, -1: none
+    weights: object   # [tokens, top_k]
+    offsets: object   # [experts + 1] rows of each expert; None without a plan
+    src: object       # [tokens * top_k] token * top_k + slot of each row, -1 past the last
+    pos: object       # [tokens, top_k] row of each slot, -1: none
 
 
 _lib = None
@@ -125,6 +181,19 @@ def load(path: str = None) -> ctypes.CDLL:
     lib.muon_debug_build.restype = ctypes.c_int
     lib.muon_debug_guard_check.argtypes = [vp, ctypes.POINTER(ctypes.c_int64)]
     lib.muon_debug_guard_check.restype = i32
+    for name, args in (
+            ("muon_rmsnorm_forward", [ctypes.POINTER(RmsNorm), vp]),
+            ("muon_rmsnorm_backward", [ctypes.POINTER(RmsNormGrad), vp]),
+            ("muon_route_forward", [ctypes.POINTER(RouteConfig), vp, i32, i64, i64, vp, vp, vp, vp,
+                                    vp, vp, vp, vp]),
+            ("muon_route_plan", [vp, i64, i32, i32, vp, vp, vp, vp]),
+            ("muon_route_backward", [ctypes.POINTER(RouteConfig), vp, i32, i64, i64, vp, vp, vp,
+                                     i64, vp]),
+            ("muon_experts_forward", [ctypes.POINTER(Experts), vp, i64, vp, vp]),
+            ("muon_experts_backward", [ctypes.POINTER(Experts), vp, i64, vp, vp, i64, vp, vp, i32,
+                                       vp, vp])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, i32
     lib.muon_query_status.argtypes = [vp]
     lib.muon_query_status.restype = i32
     lib.muon_status_string.argtypes = [i32]
@@ -376,3 +445,256 @@ def muon_assign_owners(costs, n_ranks: int, nbytes=None, elems=None, layers=None
     out = (ctypes.c_int32 * max(1, n))()
     check(load().muon_assign_owners(arr, n, n_ranks, eps, out), "muon_assign_owners")
     return [out[i] for i in range(n)]
+
+
+# ---- the mixture-of-experts block ------------------------------------------------------
+def _codes():
+    import torch
+    return {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16, torch.float8_e4m3fn: MUON_E4M3}
+
+
+_DTYPE_CODES = None
+
+
+def _code(dtype) -> int:
+    global _DTYPE_CODES
+    if _DTYPE_CODES is None:
+        _DTYPE_CODES = _codes()
+    try:
+        return _DTYPE_CODES[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {dtype}") from None
+
+
+def _rows(t, name: str, cols: Optional[int] = None, rows: Optional[int] = None):
+    """(pointer, row stride, dtype code) of a CUDA tensor [..., cols] whose
+    leading dimensions are one run of rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, cols]")
+    r, c = t.shape
+    if (cols is not None and c != cols) or (rows is not None and r != rows):
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected {(rows, cols)}")
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: neighbouring columns must be adjacent in memory")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    stride = t.stride(0) if r > 1 else c
+    if r > 1 and stride < c:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), stride, _code(t.dtype)
+
+
+def _dense(t, name: str, shape, dtype) -> int:
+    """Pointer of a contiguous CUDA tensor of exactly this shape and dtype."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def muon_rmsnorm_forward(x, gain=None, residual=None, eps: float = 1e-6, y_dtype=None, group: int = 0,
+                         h=None, y=None, scales=None, stream=None):
+    """(y, h, scales) of h = x + residual, y = gain h / sqrt(mean(h^2) + eps)
+    for CUDA tensors [rows, cols]; see include/muon.h.
+
+    y has dtype `y_dtype` (x's by default; float8_e4m3fn adds `scales`, one per
+    row or, with group = 128, per 128 columns).  h has the residual's dtype; it
+    is None without a residual unless given.  Outputs that are not given are
+    allocated; h may be `residual` itself."""
+    import torch
+    rows, cols = x.shape
+    a = RmsNorm(rows=rows, cols=cols, eps=eps, group=group)
+    a.x, a.x_stride, a.x_dtype = _rows(x, "x")
+    if residual is not None:
+        a.residual, a.residual_stride, a.residual_dtype = _rows(residual, "residual", cols, rows)
+        if h is None:
+            h = torch.empty((rows, cols), dtype=residual.dtype, device=x.device)
+    if gain is not None:
+        a.gain, a.gain_dtype = _dense(gain, "gain", (cols,), gain.dtype), _code(gain.dtype)
+    if h is not None:
+        a.h, a.h_stride, a.h_dtype = _rows(h, "h", cols, rows)
+    if y is None:
+        y = torch.empty((rows, cols), dtype=y_dtype or x.dtype, device=x.device)
+    elif y_dtype is not None and y.dtype != y_dtype:
+        raise ValueError(f"y is {y.dtype}, expected {y_dtype}")
+    a.y, a.y_stride, a.y_dtype = _rows(y, "y", cols, rows)
+    if a.y_dtype == MUON_E4M3:
+        n = -(-cols // group) if group > 0 else 1
+        if scales is None:
+            scales = torch.empty((rows, n), dtype=torch.float32, device=x.device)
+        a.scales = _dense(scales, "scales", (rows, n), torch.float32)
+    else:
+        scales = None
+    check(load().muon_rmsnorm_forward(ctypes.byref(a), _stream_ptr(stream)), "muon_rmsnorm_forward")
+    return y, h, scales
+
+
+def muon_rmsnorm_backward(dy, h, gain=None, dres=None, eps: float = 1e-6, dh=None, dgain=None,
+                          want_dgain: bool = True, stream=None):
+    """(dh, dgain) of muon_rmsnorm_forward: dh (h's dtype unless given) is the
+    gradient of x and of the residual, with `dres`, the gradient that reaches
+    h along the residual stream, added; dgain is f32 [cols] (None when not
+    wanted)."""
+    import torch
+    rows, cols = dy.shape
+    a = RmsNormGrad(rows=rows, cols=cols, eps=eps)
+    a.dy, a.dy_stride, a.dy_dtype = _rows(dy, "dy")
+    a.h, a.h_stride, a.h_dtype = _rows(h, "h", cols, rows)
+    if gain is not None:
+        a.gain, a.gain_dtype = _dense(gain, "gain", (cols,), gain.dtype), _code(gain.dtype)
+    if dres is not None:
+        a.dres, a.dres_stride, a.dres_dtype = _rows(dres, "dres", cols, rows)
+    if dh is None:
+        dh = torch.empty((rows, cols), dtype=h.dtype, device=dy.device)
+    a.dh, a.dh_stride, a.dh_dtype = _rows(dh, "dh", cols, rows)
+    if dgain is None and want_dgain:
+        dgain = torch.empty(cols, dtype=torch.float32, device=dy.device)
+    if dgain is not None:
+        a.dgain = _dense(dgain, "dgain", (cols,), torch.float32)
+    check(load().muon_rmsnorm_backward(ctypes.byref(a), _stream_ptr(stream)), "muon_rmsnorm_backward")
+    return dh, dgain
+
+
+def make_route_config(experts: int, top_k: int, score: int = ROUTE_SOFTMAX, groups: int = 1,
+                      top_groups: Optional[int] = None, group_score: int = GROUP_MAX,
+                      renormalize: bool = False, scale: float = 1.0) -> RouteConfig:
+    """Build a RouteConfig (include/muon.h); top_groups defaults to every group."""
+    return RouteConfig(experts, top_k, score, groups, groups if top_groups is None else top_groups,
+                       group_score, int(renormalize), scale)
+
+
+def _plan_tensors(tokens: int, top_k: int, experts: int, device):
+    import torch
+    return (torch.empty(experts + 1, dtype=torch.int32, device=device),
+            torch.empty(tokens * top_k, dtype=torch.int32, device=device),
+            torch.empty((tokens, top_k), dtype=torch.int32, device=device))
+
+
+def muon_route_forward(logits, cfg: RouteConfig, bias=None, mask=None, plan: bool = True,
+                       stream=None) -> Route:
+    """Experts and weights of every token from CUDA logits [tokens, experts]
+    (f32 or bf16), and their rows in expert order unless `plan` is false.
+    bias: f32 [experts], seen by the choice only.  mask: bool or uint8
+    [tokens], tokens to leave out are false."""
+    import torch
+    ptr, stride, code = _rows(logits, "logits", cfg.experts)
+    tokens, dev = logits.shape[0], logits.device
+    idx = torch.empty((tokens, cfg.top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((tokens, cfg.top_k), dtype=torch.float32, device=dev)
+    off = src = pos = None
+    if plan:
+        off, src, pos = _plan_tensors(tokens, cfg.top_k, cfg.experts, dev)
+    b = _dense(bias, "bias", (cfg.experts,), torch.float32) if bias is not None else None
+    m = None
+    if mask is not None:
+        m = _dense(mask, "mask", (tokens,), torch.bool if mask.dtype == torch.bool else torch.uint8)
+    check(load().muon_route_forward(
+        ctypes.byref(cfg), ptr, code, stride, tokens, b, m, idx.data_ptr(), weights.data_ptr(),
+        off.data_ptr() if plan else None, src.data_ptr() if plan else None,
+        pos.data_ptr() if plan else None, _stream_ptr(stream)), "muon_route_forward")
+    return Route(idx, weights, off, src, pos)
+
+
+def muon_route_plan(idx, experts: int, stream=None):
+    """(offsets, src, pos) of int32 CUDA idx [tokens, top_k]: the pairs' rows in expert order."""
+    import torch
+    tokens, top_k = idx.shape
+    p = _dense(idx, "idx", (tokens, top_k), torch.int32)
+    off, src, pos = _plan_tensors(tokens, top_k, experts, idx.device)
+    check(load().muon_route_plan(p, tokens, top_k, experts, off.data_ptr(), src.data_ptr(),
+                                 pos.data_ptr(), _stream_ptr(stream)), "muon_route_plan")
+    return off, src, pos
+
+
+def muon_route_backward(logits, cfg: RouteConfig, idx, dweights, dlogits=None, stream=None):
+    """Gradient of the routing weights with respect to the logits (their dtype)."""
+    import torch
+    ptr, stride, code = _rows(logits, "logits", cfg.experts)
+    tokens = logits.shape[0]
+    if dlogits is None:
+        dlogits = torch.empty((tokens, cfg.experts), dtype=logits.dtype, device=logits.device)
+    dptr, dstride, dcode = _rows(dlogits, "dlogits", cfg.experts, tokens)
+    if dcode != code:
+        raise ValueError("dlogits must have the logits' dtype")
+    i = _dense(idx, "idx", (tokens, cfg.top_k), torch.int32)
+    w = _dense(dweights, "dweights", (tokens, cfg.top_k), torch.float32)
+    check(load().muon_route_backward(ctypes.byref(cfg), ptr, code, stride, tokens, i, w, dptr, dstride,
+                                     _stream_ptr(stream)), "muon_route_backward")
+    return dlogits
+
+
+def _experts_args(x, w_in, w_out, route: Route):
+    import torch
+    if w_out.dim() != 3:
+        raise ValueError("w_out must be [experts, hidden, inner]")
+    experts, hidden, inner = w_out.shape
+    bf16, i32 = torch.bfloat16, torch.int32
+    if x.dtype != bf16:
+        raise TypeError(f"x must be bfloat16, got {x.dtype}")
+    ptr, stride, _ = _rows(x, "x", hidden)
+    tokens, top_k = x.shape[0], route.weights.shape[1]
+    if route.offsets is None:
+        raise ValueError("the routing has no plan")
+    return Experts(
+        tokens, hidden, inner, experts, top_k, ptr, stride,
+        _dense(w_in, "w_in", (experts, 2 * inner, hidden), bf16),
+        _dense(w_out, "w_out", (experts, hidden, inner), bf16),
+        _dense(route.weights, "weights", (tokens, top_k), torch.float32),
+        _dense(route.offsets, "offsets", (experts + 1,), i32),
+        _dense(route.src, "src", (tokens * top_k,), i32),
+        _dense(route.pos, "pos", (tokens, top_k), i32))
+
+
+def muon_experts_forward(x, w_in, w_out, route: Route, save: bool = False, out=None, stream=None):
+    """(out, gu): out[t] = sum over slots of weight * W_out silu(W_gate x) (W_up x)
+    for bf16 CUDA x [tokens, hidden], w_in [experts, 2 * inner, hidden] (gate
+    rows, then up rows), w_out [experts, hidden, inner].  gu, what
+    muon_experts_backward needs, is None unless `save`."""
+    import torch
+    a = _experts_args(x, w_in, w_out, route)
+    if out is None:
+        out = torch.empty((a.tokens, a.hidden), dtype=torch.bfloat16, device=x.device)
+    elif out.dtype != torch.bfloat16:
+        raise TypeError(f"out must be bfloat16, got {out.dtype}")
+    optr, ostride, _ = _rows(out, "out", a.hidden, a.tokens)
+    gu = None
+    if save:
+        gu = torch.empty((a.tokens * a.top_k, 2 * a.inner), dtype=torch.bfloat16, device=x.device)
+    check(load().muon_experts_forward(ctypes.byref(a), optr, ostride,
+                                      gu.data_ptr() if save else None, _stream_ptr(stream)),
+          "muon_experts_forward")
+    return out, gu
+
+
+def muon_experts_backward(dout, x, w_in, w_out, route: Route, gu, dw_dtype=None, dx=None, dw_in=None,
+                          dw_out=None, want_dx: bool = True, want_dw: bool = True, stream=None):
+    """(dx, dw_in, dw_out, dweights) of muon_experts_forward.  The weights'
+    gradients have dtype `dw_dtype` (f32 by default, or bf16) and the weights'
+    shapes, as muon_step_grouped takes them; dweights is f32 [tokens, top_k]
+    for muon_route_backward."""
+    import torch
+    a = _experts_args(x, w_in, w_out, route)
+    bf16 = torch.bfloat16
+    if dout.dtype != bf16 or (dx is not None and dx.dtype != bf16):
+        raise TypeError("dout and dx must be bfloat16")
+    dptr, dstride, _ = _rows(dout, "dout", a.hidden, a.tokens)
+    g = _dense(gu, "gu", (a.tokens * a.top_k, 2 * a.inner), bf16)
+    xptr, xstride = None, a.hidden
+    if dx is None and want_dx:
+        dx = torch.empty((a.tokens, a.hidden), dtype=bf16, device=x.device)
+    if dx is not None:
+        xptr, xstride, _ = _rows(dx, "dx", a.hidden, a.tokens)
+    if want_dw:
+        dw_dtype = dw_dtype or (dw_in.dtype if dw_in is not None else torch.float32)
+        if dw_in is None:
+            dw_in = torch.empty(w_in.shape, dtype=dw_dtype, device=x.device)
+        if dw_out is None:
+            dw_out = torch.empty(w_out.shape, dtype=dw_dtype, device=x.device)
+    code = _code(dw_dtype) if dw_dtype is not None else MUON_F32
+    dweights = torch.empty((a.tokens, a.top_k), dtype=torch.float32, device=x.device)
+    check(load().muon_experts_backward(
+        ctypes.byref(a), dptr, dstride, g, xptr, xstride,
+        _dense(dw_in, "dw_in", w_in.shape, dw_dtype) if want_dw else None,
+        _dense(dw_out, "dw_out", w_out.shape, dw_dtype) if want_dw else None,
+        code, dweights.data_ptr(), _stream_ptr(stream)), "muon_experts_backward")
+    return dx, dw_in, dw_out, dweights

@@ -21,6 +21,7 @@
 #include <vector>
 
 #include "../../include/muon.h"
+#include "block.h"
 #include "muon_internal.h"
 
 using namespace muon;
@@ -1515,6 +1516,27 @@ int take_injected_stall(int kind) {
   int want = kind;
   return g_inject.compare_exchange_strong(want, 0) ? 1 : 0;
 }
+
+// State shared with the mixture-of-experts block's entry points (block_api.cpp).
+std::mutex& api_mutex() { return g_mu; }
+
+int api_device(ApiDevice* out) {
+  DevState* d = nullptr;
+  const muon_status_t st = dev_state(&d);
+  if (st != MUON_OK) return st;
+  out->sms = d->sms;
+  out->status = d->status;
+  out->timeout_ns =
+      static_cast<unsigned long long>(env_size("MUON_WAIT_TIMEOUT_MS", 2000)) * 1000000ull;
+  return MUON_OK;
+}
+
+int api_workspace(cudaStream_t stream, size_t bytes, char** out) {
+  unsigned* ctr = nullptr;
+  return get_workspace(stream, bytes, 1, out, &ctr);
+}
+
+void api_set_launches(int n) { t_last_launches = n; }
 }  // namespace muon
 
 extern "C" {
