@@ -111,48 +111,81 @@ cudaError_t launch_plan_hist(const PlanParams& p, cudaStream_t s);
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t s);
 
 // ---- experts' products ---------------------------------------------------------------------
-struct ExpertsParams {
-  int64_t tokens, hidden, inner, rows;   // rows = tokens * top_k
-  int experts, top_k;
-  const __nv_bfloat16* x;
-  int64_t xs;
-  const __nv_bfloat16* w_in;
-  const __nv_bfloat16* w_out;
-  const float* weights;
-  const int32_t* offsets;
-  const int32_t* src;
-  const int32_t* pos;
-  // forward
-  __nv_bfloat16* gu;        // [rows][2 inner]
-  __nv_bfloat16* act;       // [rows][inner]
-  __nv_bfloat16* y;         // [rows][hidden]
-  __nv_bfloat16* out;
-  int64_t outs;
-  // backward
-  const __nv_bfloat16* dout;
-  int64_t dos;
-  const __nv_bfloat16* gu_in;
-  float* da;                // [rows][inner]
-  __nv_bfloat16* dgu;       // [rows][2 inner]
-  __nv_bfloat16* wact;      // [rows][inner]
-  __nv_bfloat16* dxr;       // [rows][hidden]
-  __nv_bfloat16* dx;
-  int64_t dxs;
-  void* dw_in;
-  void* dw_out;
-  int dw_dt;
-  float* dweights;
+// Products on the tensor cores (experts.cu), by operand and result.
+enum ExKind : int {
+  kExUp = 0,     // rows x W_in^T  -> act (and gate, up)
+  kExDown = 1,   // act  x W_out^T -> y
+  kExDact = 2,   // dout x W_out   -> dgu, w a, dweights' parts
+  kExDx = 3,     // dgu  x W_in    -> y
+  kExDwIn = 4,   // dgu^T  x rows
+  kExDwOut = 5   // dout^T x w a
+};
+constexpr int kExSeg = 64;        // row segments of the gradient's buffers: a K block
+constexpr int kExMTile = 256;     // rows of the weight-side dimension per CTA pair
+constexpr int kExNTile = 256;     // most token rows (gradients: columns) per CTA pair
+
+struct ExGemmParams {
+  CUtensorMap mapA, mapB;         // weight-side and token-side operand
+  const int32_t* offsets;         // [experts + 1]
+  int64_t rows;                   // tokens * top_k, the most rows there are
+  int experts;
+  int pad;                        // padded row numbering: segments of 1 or kExSeg rows
+  int m_tiles, n_tiles;           // M tiles of a pair; kExDw*: N tiles
+  int kb;                         // K blocks of 64 (kExDw*: from the expert's rows)
+  int m, n;                       // valid M (padded for kExDwIn) and, kExDw*, N
+  int inner, ip;                  // inner, and rounded up to 8
+  __nv_bfloat16* act;             // [padded rows][ip]: kExUp act, kExDact w a
+  __nv_bfloat16* gu;              // [rows][2 inner]: kExUp output or null, kExDact input
+  int gu_vec;                     // 16-byte accesses to gu are legal
+  float* y;                       // [rows][yp]
+  int64_t yp;
+  const float* wr;                // [padded rows] weight of a row
+  __nv_bfloat16* dgu;             // [padded rows][2 ip]
+  float* part;                    // [m_tiles * 8][rows] parts of dweights
+  void* dw;
+  int dw_dt, dw_vec;
+  unsigned* status;
+  unsigned long long timeout_ns;
 };
 
-cudaError_t launch_experts_gu(const ExpertsParams& p, cudaStream_t s);
-cudaError_t launch_experts_act(const ExpertsParams& p, cudaStream_t s);
-cudaError_t launch_experts_down(const ExpertsParams& p, cudaStream_t s);
-cudaError_t launch_experts_da(const ExpertsParams& p, cudaStream_t s);
-cudaError_t launch_experts_dact(const ExpertsParams& p, cudaStream_t s);
-cudaError_t launch_experts_dx(const ExpertsParams& p, cudaStream_t s);
-cudaError_t launch_experts_dw(const ExpertsParams& p, bool w_out, cudaStream_t s);
-// out[t] = sum_j (weighted ? weights[t,j] : 1) rows[pos[t,j]]
-cudaError_t launch_experts_combine(const ExpertsParams& p, const __nv_bfloat16* rows, bool weighted,
-                                   __nv_bfloat16* out, int64_t outs, cudaStream_t s);
+// Rows of x (and dout) in expert order, zero rows up to each segment's end.
+struct ExGatherParams {
+  const __nv_bfloat16* x[2];      // x, dout or null
+  int64_t xs[2];
+  __nv_bfloat16* out[2];          // [padded rows][hp]
+  int vec;                        // 16-byte accesses are legal
+  const float* weights;           // with wr: the row's weight
+  float* wr;
+  const int32_t* offsets;
+  const int32_t* src;
+  int64_t rows, hidden, hp;
+  int experts, top_k, pad;
+};
+
+struct ExCombineParams {          // out[t] = sum_j w[t,j] y[pos[t,j]]
+  const float* y;
+  int64_t yp;
+  const int32_t* pos;
+  const float* weights;           // null: ones
+  __nv_bfloat16* out;
+  int64_t outs, tokens, hidden, rows;
+  int top_k, vec;
+};
+
+struct ExWeightParams {           // dweights[t,j] = sum over parts of part[.][pos[t,j]]
+  const float* part;
+  const int32_t* pos;
+  float* dweights;
+  int64_t rows;
+  int parts;
+};
+
+cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, cudaStream_t s);
+cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, cudaStream_t s);
+cudaError_t launch_ex_combine(const ExCombineParams& p, cudaStream_t s);
+cudaError_t launch_ex_dweights(const ExWeightParams& p, cudaStream_t s);
+// mats matrices [rows][cols] -> [rows_p][cols_p], zeros around
+cudaError_t launch_ex_repack(const __nv_bfloat16* in, int64_t mats, int64_t rows, int64_t cols,
+                             __nv_bfloat16* out, int64_t rows_p, int64_t cols_p, cudaStream_t s);
 
 }  // namespace muon

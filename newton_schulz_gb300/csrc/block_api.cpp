@@ -347,17 +347,111 @@ bool experts_alias(const ExpertsViews& v, std::initializer_list<View> more_input
   return false;
 }
 
-ExpertsParams experts_params(const muon_experts_t* a) {
-  ExpertsParams p;
+int64_t rup(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Workspace, cut into 256-byte aligned pieces: sizes first, then pointers.
+struct Carve {
+  size_t bytes = 0;
+  size_t take(int64_t n) {
+    const size_t at = bytes;
+    bytes += pad256(static_cast<size_t>(n));
+    return at;
+  }
+};
+
+// The weights as the tensor maps want them: rows of a multiple of 8 elements
+// on 16-byte boundaries, inner a multiple of 8 (gate and up rows interleave
+// by 8).  Others are copied into the workspace with zeros around.
+struct WeightPlan {
+  int64_t hp, ip;            // hidden and inner rounded up to 8
+  bool pack_in, pack_out;
+  size_t at_in, at_out;
+  WeightPlan(const muon_experts_t* a, Carve* c)
+      : hp(rup(a->hidden, 8)),
+        ip(rup(a->inner, 8)),
+        pack_in(hp != a->hidden || ip != a->inner || !aligned(a->w_in, 16)),
+        pack_out(ip != a->inner || !aligned(a->w_out, 16)) {
+    at_in = pack_in ? c->take(2LL * a->experts * ip * hp * 2) : 0;
+    at_out = pack_out ? c->take(static_cast<int64_t>(a->experts) * a->hidden * ip * 2) : 0;
+  }
+};
+
+muon_status_t pack_weights(const muon_experts_t* a, const WeightPlan& w, char* ws, const __nv_bfloat16** w_in,
+                           const __nv_bfloat16** w_out, Counter* c, cudaStream_t s) {
+  *w_in = static_cast<const __nv_bfloat16*>(a->w_in);
+  *w_out = static_cast<const __nv_bfloat16*>(a->w_out);
+  if (w.pack_in) {
+    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(ws + w.at_in);
+    MUON_TRY(c->run(launch_ex_repack(*w_in, 2LL * a->experts, a->inner, a->hidden, o, w.ip, w.hp, s)));
+    *w_in = o;
+  }
+  if (w.pack_out) {
+    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(ws + w.at_out);
+    MUON_TRY(c->run(launch_ex_repack(*w_out, a->experts, a->hidden, a->inner, o, a->hidden, w.ip, s)));
+    *w_out = o;
+  }
+  return MUON_OK;
+}
+
+// [d2][d1][d0] bf16 with row pitch `pitch` (elements), box b0 x b1.
+bool map3(CUtensorMap* m, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t pitch, uint32_t b1) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(d0), static_cast<uint64_t>(d1), static_cast<uint64_t>(d2)};
+  const uint64_t st[2] = {static_cast<uint64_t>(pitch * 2), static_cast<uint64_t>(pitch * d1 * 2)};
+  const uint32_t box[3] = {64, b1, 1};
+  return encode_bf16_nd(m, base, 3, dims, st, box);
+}
+bool map2(CUtensorMap* m, const void* base, int64_t d0, int64_t d1, int64_t pitch, uint32_t b1) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(d0), static_cast<uint64_t>(d1)};
+  const uint64_t st[1] = {static_cast<uint64_t>(pitch * 2)};
+  const uint32_t box[2] = {64, b1};
+  return encode_bf16_nd(m, base, 2, dims, st, box);
+}
+// W_in as [e][ip / 8][gate, up][8][hidden]: a box of 64 x 8 x 2 x 8 is 128
+// rows, 8 gate rows and 8 up rows in turn.
+bool map_up(CUtensorMap* m, const void* base, const muon_experts_t* a, const WeightPlan& w) {
+  const uint64_t row = static_cast<uint64_t>(w.hp) * 2;
+  const uint64_t dims[5] = {static_cast<uint64_t>(a->hidden), 8, 2, static_cast<uint64_t>(w.ip / 8),
+                            static_cast<uint64_t>(a->experts)};
+  const uint64_t st[4] = {row, row * w.ip, row * 8, row * 2 * w.ip};
+  const uint32_t box[5] = {64, 8, 2, 8, 1};
+  return encode_bf16_nd(m, base, 5, dims, st, box);
+}
+
+ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const ApiDevice& d, int pad) {
+  ExGemmParams p;
   std::memset(&p, 0, sizeof(p));
-  p.tokens = a->tokens, p.hidden = a->hidden, p.inner = a->inner, p.rows = a->tokens * a->top_k;
-  p.experts = a->experts, p.top_k = a->top_k;
-  p.x = static_cast<const __nv_bfloat16*>(a->x), p.xs = a->x_stride;
-  p.w_in = static_cast<const __nv_bfloat16*>(a->w_in);
-  p.w_out = static_cast<const __nv_bfloat16*>(a->w_out);
-  p.weights = a->weights, p.offsets = a->offsets, p.src = a->src, p.pos = a->pos;
+  p.offsets = a->offsets;
+  p.rows = a->tokens * a->top_k;
+  p.experts = a->experts;
+  p.pad = pad;
+  p.inner = static_cast<int>(a->inner), p.ip = static_cast<int>(w.ip);
+  p.status = d.status, p.timeout_ns = d.timeout_ns;
   return p;
 }
+
+ExGatherParams gather_params(const muon_experts_t* a, const WeightPlan& w, int pad) {
+  ExGatherParams g;
+  std::memset(&g, 0, sizeof(g));
+  g.x[0] = static_cast<const __nv_bfloat16*>(a->x), g.xs[0] = a->x_stride;
+  g.offsets = a->offsets, g.src = a->src;
+  g.rows = a->tokens * a->top_k, g.hidden = a->hidden, g.hp = w.hp;
+  g.experts = a->experts, g.top_k = a->top_k, g.pad = pad;
+  return g;
+}
+
+ExCombineParams combine_params(const muon_experts_t* a, const float* y, int64_t yp, const float* weights,
+                               const View& out) {
+  ExCombineParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.y = y, p.yp = yp, p.pos = a->pos, p.weights = weights;
+  p.out = static_cast<__nv_bfloat16*>(const_cast<void*>(out.p));
+  p.outs = out.stride, p.tokens = a->tokens, p.hidden = a->hidden, p.rows = a->tokens * a->top_k;
+  p.top_k = a->top_k;
+  p.vec = aligned(out.p, 8) && (out.rows <= 1 || out.stride % 4 == 0);
+  return p;
+}
+
+int tiles_of(int64_t n, int64_t per) { return static_cast<int>((n + per - 1) / per); }
 
 muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, void* gu, cudaStream_t stream) {
   ExpertsViews v;
@@ -367,25 +461,43 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
     api_set_launches(0);
     return MUON_OK;
   }
-  const int64_t rows = a->tokens * a->top_k;
-  const View o{out, MUON_BF16, a->tokens, a->hidden, outs}, og = dense(gu, MUON_BF16, rows * 2 * a->inner);
+  const int64_t rows = a->tokens * a->top_k, H = a->hidden, I = a->inner;
+  const View o{out, MUON_BF16, a->tokens, H, outs}, og = dense(gu, MUON_BF16, rows * 2 * I);
   if (!out || o.bad_stride() || !aligned(out, 2) || !aligned(gu, 2)) return MUON_ERR_INVALID_ARGUMENT;
   if (experts_alias(v, {}, {o, og})) return MUON_ERR_ALIAS;
-  ExpertsParams p = experts_params(a);
   std::lock_guard<std::mutex> lock(api_mutex());
-  const size_t n_gu = gu ? 0 : pad256(static_cast<size_t>(rows * 2 * a->inner) * 2),
-               n_act = pad256(static_cast<size_t>(rows * a->inner) * 2),
-               n_y = pad256(static_cast<size_t>(rows * a->hidden) * 2);
+  ApiDevice d;
+  MUON_TRY(device(&d));
+  Carve cv;
+  const WeightPlan w(a, &cv);
+  const int64_t yp = rup(H, 4);
+  const size_t at_x = cv.take(rows * w.hp * 2), at_act = cv.take(rows * w.ip * 2), at_y = cv.take(rows * yp * 4);
   char* ws = nullptr;
-  MUON_TRY(workspace(stream, n_gu + n_act + n_y, &ws));
-  p.gu = static_cast<__nv_bfloat16*>(gu ? gu : ws);
-  p.act = reinterpret_cast<__nv_bfloat16*>(ws + n_gu);
-  p.y = reinterpret_cast<__nv_bfloat16*>(ws + n_gu + n_act);
+  MUON_TRY(workspace(stream, cv.bytes, &ws));
+  __nv_bfloat16* xp = reinterpret_cast<__nv_bfloat16*>(ws + at_x);
+  __nv_bfloat16* act = reinterpret_cast<__nv_bfloat16*>(ws + at_act);
+  float* y = reinterpret_cast<float*>(ws + at_y);
   Counter c;
-  MUON_TRY(c.run(launch_experts_gu(p, stream)));
-  MUON_TRY(c.run(launch_experts_act(p, stream)));
-  MUON_TRY(c.run(launch_experts_down(p, stream)));
-  MUON_TRY(c.run(launch_experts_combine(p, p.y, true, static_cast<__nv_bfloat16*>(out), outs, stream)));
+  const __nv_bfloat16 *w_in, *w_out;
+  MUON_TRY(pack_weights(a, w, ws, &w_in, &w_out, &c, stream));
+  ExGatherParams g = gather_params(a, w, 1);
+  g.out[0] = xp;
+  g.vec = v.x.rows16();
+  MUON_TRY(c.run(launch_ex_gather(g, rows, stream)));
+  ExGemmParams up = gemm_params(a, w, d, 1);
+  up.m_tiles = tiles_of(2 * w.ip, kExMTile), up.kb = tiles_of(H, 64), up.m = up.inner;
+  up.act = act;
+  up.gu = static_cast<__nv_bfloat16*>(gu);
+  up.gu_vec = aligned(gu, 16) && I % 8 == 0;
+  ExGemmParams down = gemm_params(a, w, d, 1);
+  down.m_tiles = tiles_of(H, kExMTile), down.kb = tiles_of(I, 64), down.m = static_cast<int>(H);
+  down.y = y, down.yp = yp;
+  if (!map_up(&up.mapA, w_in, a, w) || !map2(&up.mapB, xp, H, rows, w.hp, 32) ||
+      !map3(&down.mapA, w_out, I, H, a->experts, w.ip, 128) || !map2(&down.mapB, act, I, rows, w.ip, 32))
+    return MUON_ERR_CUDA;
+  MUON_TRY(c.run(launch_ex_gemm(kExUp, up, d.sms, stream)));
+  MUON_TRY(c.run(launch_ex_gemm(kExDown, down, d.sms, stream)));
+  MUON_TRY(c.run(launch_ex_combine(combine_params(a, y, yp, a->weights, o), stream)));
   api_set_launches(c.n);
   return MUON_OK;
 }
@@ -397,15 +509,14 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   bool empty = false;
   MUON_TRY(check_experts(a, &v, &empty));
   if (!is_float_dtype(dw_dt)) return MUON_ERR_INVALID_ARGUMENT;
-  const int64_t rows = a->tokens * a->top_k, per = a->inner * a->hidden;
-  const View vd{dout, MUON_BF16, a->tokens, a->hidden, dos}, vg = dense(gu, MUON_BF16, rows * 2 * a->inner),
-             ox{dx, MUON_BF16, a->tokens, a->hidden, dxs}, oi = dense(dw_in, dw_dt, 2 * per * a->experts),
+  const int64_t rows = a->tokens * a->top_k, H = a->hidden, I = a->inner, per = I * H;
+  const View vd{dout, MUON_BF16, a->tokens, H, dos}, vg = dense(gu, MUON_BF16, rows * 2 * I),
+             ox{dx, MUON_BF16, a->tokens, H, dxs}, oi = dense(dw_in, dw_dt, 2 * per * a->experts),
              oo = dense(dw_out, dw_dt, per * a->experts), ow = dense(dweights, MUON_F32, rows);
   for (const View* o : {&vd, &vg, &ox, &oi, &oo, &ow})
     if (o->p && (o->bad_stride() || !aligned(o->p, esize(o->dt)))) return MUON_ERR_INVALID_ARGUMENT;
   if (!empty && (!dout || !gu)) return MUON_ERR_INVALID_ARGUMENT;
   if (experts_alias(v, {vd, vg}, {ox, oi, oo, ow})) return MUON_ERR_ALIAS;
-  Counter c;
   if (empty) {   // no rows: zero weight gradients
     for (const View* o : {&oi, &oo})
       if (o->p && cudaMemsetAsync(const_cast<void*>(o->p), 0, static_cast<size_t>(o->cols * esize(o->dt)),
@@ -414,32 +525,71 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
     api_set_launches(0);
     return MUON_OK;
   }
-  ExpertsParams p = experts_params(a);
-  p.dout = static_cast<const __nv_bfloat16*>(dout), p.dos = dos;
-  p.gu_in = static_cast<const __nv_bfloat16*>(gu);
-  p.dx = static_cast<__nv_bfloat16*>(dx), p.dxs = dxs;
-  p.dw_in = dw_in, p.dw_out = dw_out, p.dw_dt = dw_dt, p.dweights = dweights;
   std::lock_guard<std::mutex> lock(api_mutex());
-  const size_t n_da = pad256(static_cast<size_t>(rows * a->inner) * 4),
-               n_dgu = pad256(static_cast<size_t>(rows * 2 * a->inner) * 2),
-               n_wa = pad256(static_cast<size_t>(rows * a->inner) * 2),
-               n_dx = dx ? pad256(static_cast<size_t>(rows * a->hidden) * 2) : 0;
+  ApiDevice d;
+  MUON_TRY(device(&d));
+  Carve cv;
+  const WeightPlan w(a, &cv);
+  const int64_t yp = rup(H, 4);
+  // padded rows: every expert with rows adds at most kExSeg - 1
+  const int64_t prows = rows + (kExSeg - 1) * std::min<int64_t>(a->experts, rows);
+  const int parts = tiles_of(I, kExMTile) * 8;
+  const size_t at_x = cv.take(prows * w.hp * 2), at_d = cv.take(prows * w.hp * 2), at_wr = cv.take(prows * 4),
+               at_dgu = cv.take(prows * 2 * w.ip * 2), at_wa = cv.take(prows * w.ip * 2),
+               at_part = cv.take(rows * parts * 4), at_y = dx ? cv.take(rows * yp * 4) : 0;
   char* ws = nullptr;
-  MUON_TRY(workspace(stream, n_da + n_dgu + n_wa + n_dx, &ws));
-  p.da = reinterpret_cast<float*>(ws);
-  p.dgu = reinterpret_cast<__nv_bfloat16*>(ws + n_da);
-  p.wact = reinterpret_cast<__nv_bfloat16*>(ws + n_da + n_dgu);
-  p.dxr = reinterpret_cast<__nv_bfloat16*>(ws + n_da + n_dgu + n_wa);
-  if (dweights && cudaMemsetAsync(dweights, 0, static_cast<size_t>(rows) * 4, stream) != cudaSuccess)
+  MUON_TRY(workspace(stream, cv.bytes, &ws));
+  __nv_bfloat16* xp = reinterpret_cast<__nv_bfloat16*>(ws + at_x);
+  __nv_bfloat16* dop = reinterpret_cast<__nv_bfloat16*>(ws + at_d);
+  __nv_bfloat16* dgu = reinterpret_cast<__nv_bfloat16*>(ws + at_dgu);
+  __nv_bfloat16* wact = reinterpret_cast<__nv_bfloat16*>(ws + at_wa);
+  Counter c;
+  const __nv_bfloat16 *w_in, *w_out;
+  MUON_TRY(pack_weights(a, w, ws, &w_in, &w_out, &c, stream));
+  ExGatherParams g = gather_params(a, w, kExSeg);
+  if (!dw_in) g.x[0] = nullptr;
+  g.out[0] = xp;
+  g.x[1] = static_cast<const __nv_bfloat16*>(dout), g.xs[1] = dos, g.out[1] = dop;
+  g.weights = a->weights;
+  g.wr = reinterpret_cast<float*>(ws + at_wr);
+  g.vec = v.x.rows16() && vd.rows16();
+  MUON_TRY(c.run(launch_ex_gather(g, prows, stream)));
+  ExGemmParams da = gemm_params(a, w, d, kExSeg);
+  da.m_tiles = tiles_of(I, kExMTile), da.kb = tiles_of(H, 64), da.m = da.inner;
+  da.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));
+  da.gu_vec = aligned(gu, 16) && I % 8 == 0;
+  da.wr = g.wr, da.dgu = dgu, da.act = wact;
+  da.part = reinterpret_cast<float*>(ws + at_part);
+  if (!map3(&da.mapA, w_out, I, H, a->experts, w.ip, 64) || !map2(&da.mapB, dop, H, prows, w.hp, 32))
     return MUON_ERR_CUDA;
-  MUON_TRY(c.run(launch_experts_da(p, stream)));
-  MUON_TRY(c.run(launch_experts_dact(p, stream)));
-  if (dx) {
-    MUON_TRY(c.run(launch_experts_dx(p, stream)));
-    MUON_TRY(c.run(launch_experts_combine(p, p.dxr, false, p.dx, dxs, stream)));
+  MUON_TRY(c.run(launch_ex_gemm(kExDact, da, d.sms, stream)));
+  if (dweights) {
+    const ExWeightParams wp{da.part, a->pos, dweights, rows, parts};
+    MUON_TRY(c.run(launch_ex_dweights(wp, stream)));
   }
-  if (dw_in) MUON_TRY(c.run(launch_experts_dw(p, false, stream)));
-  if (dw_out) MUON_TRY(c.run(launch_experts_dw(p, true, stream)));
+  if (dx) {
+    ExGemmParams p = gemm_params(a, w, d, kExSeg);
+    p.m_tiles = tiles_of(H, kExMTile), p.kb = tiles_of(2 * w.ip, 64), p.m = static_cast<int>(H);
+    p.y = reinterpret_cast<float*>(ws + at_y), p.yp = yp;
+    if (!map3(&p.mapA, w_in, H, 2 * w.ip, a->experts, w.hp, 64) ||
+        !map2(&p.mapB, dgu, 2 * w.ip, prows, 2 * w.ip, 32))
+      return MUON_ERR_CUDA;
+    MUON_TRY(c.run(launch_ex_gemm(kExDx, p, d.sms, stream)));
+    MUON_TRY(c.run(launch_ex_combine(combine_params(a, p.y, yp, nullptr, ox), stream)));
+  }
+  for (int k = 0; k < 2; ++k) {
+    void* out = k ? dw_out : dw_in;
+    if (!out) continue;
+    ExGemmParams p = gemm_params(a, w, d, kExSeg);
+    p.m = static_cast<int>(k ? H : 2 * w.ip), p.n = static_cast<int>(k ? I : H);
+    p.m_tiles = tiles_of(p.m, kExMTile), p.n_tiles = tiles_of(p.n, kExNTile);
+    p.dw = out, p.dw_dt = dw_dt;
+    p.dw_vec = aligned(out, 16) && p.n * esize(dw_dt) % 16 == 0;
+    if (!map2(&p.mapA, k ? dop : dgu, p.m, prows, k ? w.hp : 2 * w.ip, 64) ||
+        !map2(&p.mapB, k ? wact : xp, p.n, prows, k ? w.ip : w.hp, 64))
+      return MUON_ERR_CUDA;
+    MUON_TRY(c.run(launch_ex_gemm(k ? kExDwOut : kExDwIn, p, d.sms, stream)));
+  }
   api_set_launches(c.n);
   return MUON_OK;
 }

@@ -1,270 +1,816 @@
-// The experts' products over a routing (see muon_experts_forward): simple
-// kernels, right for every size.
+// The experts' products over a routing (definitions at muon_experts_forward).
 //
-// Rows are (token, slot) pairs in expert order; expert e has rows
-// [offsets[e], offsets[e + 1]).  Every product is a 64 x 64 output tile per
-// block, fp32 multiply-adds on operands widened from bf16.
+// Rows are (token, slot) pairs in expert order.  Each product is a grouped
+// GEMM with the weights on the tensor cores' M side and the rows on the N
+// side: N is any multiple of 32 up to 256, so an expert's rows are cut into
+// equal tiles with at most 31 columns too many in each, whatever its count
+// (a 128- or 256-row M tile would leave half a tile per expert idle).
+//
+//   up     D[f, r] = W_in[f, :] . x_r         gate and up rows interleaved by 8
+//   down   D[h, r] = W_out[h, :] . act_r
+//   dact   D[i, r] = W_out[:, i] . dout_r
+//   dx     D[h, r] = W_in[:, h] . dgu_r
+//   dw_in  D[f, h] = sum_r dgu[r, f] x[r, h]        K = the expert's rows
+//   dw_out D[h, i] = sum_r dout[r, h] (w a)[r, i]
+//
+// One CTA pair (a cluster of two) per tile of 256 (M) x N: tcgen05.mma with
+// cta_group::2, each CTA holding 128 rows of A, half of B's columns and 128
+// rows of D, so 32 KB of operands feed each SM per 128 x 256 x 64 block.  Per CTA:
+//   warp 0      TMA producer, a ring of five 32 KB stages (128-byte swizzle);
+//   warp 1      TMEM; in the pair's CTA 0 it issues the MMAs of both;
+//   warps 2..9  epilogue, two sets of four (128 TMEM lanes each) that take
+//               the accumulator's column slabs in turn.
+// Two 256-column accumulators let the epilogue of a tile overlap the next
+// tile's products.  Bound by the tensor cores where experts have hundreds of
+// rows, by HBM (every weight read once) where they have a few.
+//
+// The tile list follows from the offsets on the device: every CTA scans them
+// (one warp, a few hundred cycles), so the host needs no counts.  Offsets are
+// read as their running maximum clamped to [0, rows]: wrong ones give wrong
+// values, not accesses out of range.  Every wait is bounded; on a timeout a
+// status bit is set, copies in flight are awaited, TMEM is freed and the CTA
+// returns.
+//
+// The gradient's buffers keep each expert's rows in a segment padded to 64
+// rows with zeros: the weight gradients' K blocks then end with their
+// expert's, and no row of another expert, nor anything unwritten, is ever
+// multiplied.
+#include <algorithm>
+
 #include "block.h"
+#include "sm100_ptx.cuh"
 
 namespace muon {
 
 namespace {
 
-constexpr int TS = 64, TK = 16, kThreads = 256;
+constexpr int BK = 64, UMMA_K = 16;
+constexpr int kOpBytes = 128 * BK * 2;          // one CTA's A or B of a stage
+constexpr int kStageBytes = 2 * kOpBytes;
+constexpr int kStages = 5;
+constexpr int kSetBytes = 16 * 1024;            // epilogue staging per set
+constexpr int kBarOff = kStages * kStageBytes + 2 * kSetBytes;
+constexpr int kScanOff = kBarOff + 256;
+constexpr int kThreads = 320;
+constexpr uint32_t kTmemCols = 512;
+constexpr unsigned kFull = 0xffffffffu;
 
-enum Mode { kGu, kDown, kDa, kDx, kDwIn, kDwOut };
+constexpr bool is_dw(int kind) { return kind == kExDwIn || kind == kExDwOut; }
+constexpr bool a_mn(int kind) { return kind >= kExDact; }   // A read MN-major
 
-__device__ __forceinline__ int row_begin(const ExpertsParams& p, int e) {
-  return static_cast<int>(min(static_cast<int64_t>(max(p.offsets[e], 0)), p.rows));
-}
+int gemm_smem(int experts) { return kScanOff + 3 * (experts + 1) * 4 + 1024; }
 
-// token of a row, -1 where the plan names none
-__device__ __forceinline__ int64_t token_of(const ExpertsParams& p, int64_t row) {
-  const int32_t s = p.src[row];
-  return s >= 0 && s < p.rows ? s / p.top_k : -1;
-}
+// First row of every expert in the plan (off), in the padded numbering (poff)
+// and its number of row tiles (tt, running), by one warp.
+struct Scan {
+  int *off, *poff, *tt;    // [experts + 1]
+};
 
-__device__ __forceinline__ float bf(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
+__device__ __forceinline__ int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
-__device__ __forceinline__ float silu_parts(float g, float* slope) {
-  const float s = 1.f / (1.f + expf(-g));
-  *slope = s * (1.f + g * (1.f - s));
-  return g * s;
-}
-
-// Left operand of output row `m`, right operand of output column `n`.
-template <int MODE>
-__device__ __forceinline__ float left(const ExpertsParams& p, int64_t m, int64_t k, int64_t tok) {
-  if (MODE == kGu) return tok >= 0 ? bf(p.x, tok * p.xs + k) : 0.f;
-  if (MODE == kDown) return bf(p.act, m * p.inner + k);
-  if (MODE == kDa) return tok >= 0 ? bf(p.dout, tok * p.dos + k) : 0.f;
-  return bf(p.dgu, m * 2 * p.inner + k);
-}
-template <int MODE>
-__device__ __forceinline__ float right(const ExpertsParams& p, int64_t e, int64_t n, int64_t k) {
-  const int64_t H = p.hidden, I = p.inner;
-  if (MODE == kGu) return bf(p.w_in, (e * 2 * I + n) * H + k);
-  if (MODE == kDown) return bf(p.w_out, (e * H + n) * I + k);
-  if (MODE == kDa) return bf(p.w_out, (e * H + k) * I + n);
-  return bf(p.w_in, (e * 2 * I + k) * H + n);
-}
-
-__device__ __forceinline__ void fma_tile(const float (&a)[TK][TS + 4], const float (&b)[TK][TS + 4],
-                                         float (&acc)[4][4], int ty, int tx) {
+__device__ __forceinline__ void scan_offsets(const Scan& s, const int32_t* offsets, int experts,
+                                             int64_t rows, int pad, bool tile_pads, int lane) {
+  int top = 0, pbase = 0, tbase = 0;
+  for (int e0 = 0; e0 <= experts; e0 += 32) {
+    const int e = e0 + lane;
+    int v = e <= experts ? offsets[e] : 0;
+    v = max(0, static_cast<int>(min(static_cast<int64_t>(v), rows)));
 #pragma unroll
-  for (int k = 0; k < TK; ++k) {
-    float u[4], v[4];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kFull, v, o);
+      if (lane >= o) v = max(v, u);
+    }
+    v = max(v, top);
+    if (e <= experts) s.off[e] = v;
+    top = __shfl_sync(kFull, v, 31);
+  }
+  __syncwarp();
+  for (int e0 = 0; e0 < experts; e0 += 32) {
+    const int e = e0 + lane;
+    const int cnt = e < experts ? s.off[e + 1] - s.off[e] : 0;
+    const int pc = round_up(cnt, pad);
+    const int nt = ((tile_pads ? pc : cnt) + kExNTile - 1) / kExNTile;
+    int a = pc, b = nt;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u[i] = a[k][ty * 4 + i];
-      v[i] = b[k][tx * 4 + i];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kFull, a, o), w = __shfl_up_sync(kFull, b, o);
+      if (lane >= o) {
+        a += u;
+        b += w;
+      }
+    }
+    if (e < experts) {
+      s.poff[e] = pbase + a - pc;
+      s.tt[e] = tbase + b - nt;
+    }
+    pbase += __shfl_sync(kFull, a, 31);
+    tbase += __shfl_sync(kFull, b, 31);
+  }
+  if (lane == 0) {
+    s.poff[experts] = pbase;
+    s.tt[experts] = tbase;
+  }
+}
+
+// Largest e with v[e] <= x, for a non-decreasing v (empty experts skipped).
+__device__ __forceinline__ int find(const int* v, int experts, int x) {
+  int lo = 0, hi = experts - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (v[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+struct Tile {
+  int e, m, n;          // expert, M tile, N tile (dw)
+  int prow, urow;       // first row: padded and plan numbering
+  int rows;             // rows to write
+  int valid;            // rows of the plan among them
+  int cols;             // MMA N, a multiple of 32
+  int kb;               // K blocks
+};
+
+// Row tiles in groups of 8 per expert, M tiles outer and the group's row
+// tiles inner: the pairs running at one time share a few weight panels and a
+// few row panels, so that each comes from HBM once.
+constexpr int kRowGroup = 8;
+
+template <int KIND>
+__device__ __forceinline__ Tile decode(const ExGemmParams& p, const Scan& s, int tile) {
+  Tile t;
+  if (is_dw(KIND)) {
+    const int per = p.m_tiles * p.n_tiles;
+    t.e = tile / per;
+    const int r = tile - t.e * per;
+    t.m = r / p.n_tiles;
+    t.n = r - t.m * p.n_tiles;
+    t.prow = s.poff[t.e];
+    t.urow = s.off[t.e];
+    t.rows = t.valid = 0;
+    t.cols = kExNTile;
+    t.kb = (s.poff[t.e + 1] - t.prow) / kExSeg;
+    return t;
+  }
+  // the expert whose tiles [tt[e], tt[e + 1]) * m_tiles hold this one
+  t.e = find(s.tt, p.experts, tile / p.m_tiles);
+  const int nt = s.tt[t.e + 1] - s.tt[t.e];
+  int local = tile - s.tt[t.e] * p.m_tiles;
+  const int span = kRowGroup * p.m_tiles;
+  const int g = local / span;
+  local -= g * span;
+  const int ge = min(kRowGroup, nt - g * kRowGroup);
+  t.m = local / ge;
+  const int j = g * kRowGroup + local - t.m * ge;
+  const int cnt = s.off[t.e + 1] - s.off[t.e];
+  const int all = KIND == kExDact ? round_up(cnt, p.pad) : cnt;
+  const int size = round_up((all + nt - 1) / nt, 32);
+  t.prow = s.poff[t.e] + j * size;
+  t.urow = s.off[t.e] + j * size;
+  t.rows = max(0, min(size, all - j * size));
+  t.valid = max(0, min(size, cnt - j * size));
+  t.cols = max(32, round_up(t.rows, 32));
+  t.n = 0;
+  t.kb = p.kb;
+  return t;
+}
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                             unsigned* status, unsigned long long timeout_ns,
+                                             bool honour_abort) {
+  const uint32_t addr = ptx::smem_u32(bar);
+  if (ptx::mbar_try_wait(addr, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    if (ptx::mbar_try_wait(addr, parity)) return true;
+    if ((it & 255u) == 0) {
+      if (honour_abort && *abort_flag) return false;
+      if (ptx::globaltimer() - t0 > timeout_ns) {
+        atomicOr(status, kDevTimeout);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float lo_of(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_of(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+__device__ __forceinline__ float f(uint32_t v) { return __uint_as_float(v); }
+// 1 / (1 + exp(-g)); results are rounded to bf16, far above these functions' errors
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+// 8 bf16 at p[0..8), of which the first n exist.
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int n, bool vec) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (n <= 0) return v;
+  if (vec && n >= 8) return *reinterpret_cast<const uint4*>(p);
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = j < n ? q[j] : 0u;
+  v.x = w[0] | (w[1] << 16);
+  v.y = w[2] | (w[3] << 16);
+  v.z = w[4] | (w[5] << 16);
+  v.w = w[6] | (w[7] << 16);
+  return v;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const uint4& v, int n, bool vec) {
+  if (n <= 0) return;
+  if (vec && n >= 8) {
+    *reinterpret_cast<uint4*>(p) = v;
+    return;
+  }
+  uint16_t* q = reinterpret_cast<uint16_t*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) q[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+}
+
+// Staging of 16-byte chunks, rows of `pitch` bytes, chunk index XOR row % 8:
+// a column of eight rows and a row of eight chunks both touch all banks.
+__device__ __forceinline__ uint32_t staged(uint32_t base, int row, int chunk, int pitch) {
+  return base + row * pitch + ((chunk ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// What one warp of an epilogue set works on.
+struct EpiWarp {
+  uint32_t taddr;     // accumulator, this warp's 32 lanes
+  uint32_t stg;       // the set's staging
+  int set, q4, lane, tid;   // tid: 0..127 within the set
+  int m0;             // first M row of this CTA
+  __device__ void bar() const { ptx::named_bar(2 + set, 128); }
+};
+
+// gate rows and up rows sit 8 lanes apart, so one thread holds a pair
+__device__ __forceinline__ void epi_up(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
+  const int f0 = w.m0 >> 1;      // first feature: half of this CTA's 128 rows are gates
+  for (int c0 = w.set * 32; c0 < t.rows; c0 += 64) {
+    uint32_t r[2][16];
+    ptx::tmem_ld_16x256b_x4(w.taddr + c0, r[0]);
+    ptx::tmem_ld_16x256b_x4(w.taddr + (16u << 16) + c0, r[1]);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t a[4], g[4], u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float g0 = f(r[b][4 * i]), g1 = f(r[b][4 * i + 1]);
+        const float u0 = f(r[b][4 * i + 2]), u1 = f(r[b][4 * i + 3]);
+        a[i] = pack(g0 * sigmoid(g0) * u0, g1 * sigmoid(g1) * u1);
+        g[i] = pack(g0, g1);
+        u[i] = pack(u0, u1);
+      }
+      const int chunk = w.q4 * 2 + b;
+      ptx::stmatrix_x4_trans(staged(w.stg, w.lane, chunk, 128), a);
+      if (p.gu) {
+        ptx::stmatrix_x4_trans(staged(w.stg + 4096, w.lane, chunk, 128), g);
+        ptx::stmatrix_x4_trans(staged(w.stg + 8192, w.lane, chunk, 128), u);
+      }
+    }
+    w.bar();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int row = (w.tid >> 3) + 16 * k, chunk = w.tid & 7, ft = f0 + chunk * 8;
+      if (c0 + row >= t.rows) continue;
+      store8(p.act + static_cast<int64_t>(t.prow + c0 + row) * p.ip + ft,
+             lds16(staged(w.stg, row, chunk, 128)), p.ip - ft, true);
+      if (p.gu) {
+        __nv_bfloat16* o = p.gu + static_cast<int64_t>(t.urow + c0 + row) * 2 * p.inner + ft;
+        store8(o, lds16(staged(w.stg + 4096, row, chunk, 128)), p.inner - ft, p.gu_vec != 0);
+        store8(o + p.inner, lds16(staged(w.stg + 8192, row, chunk, 128)), p.inner - ft, p.gu_vec != 0);
+      }
+    }
+    w.bar();
+  }
+}
+
+// fp32 rows: lane = feature, so a warp's store is one full 128-byte line
+__device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
+  const int h = w.m0 + w.q4 * 32 + w.lane;
+  for (int c0 = w.set * 32; c0 < t.rows; c0 += 64) {
+    uint32_t r[32];
+    ptx::tmem_ld_32x32b_x32(w.taddr + c0, r);
+    ptx::tmem_ld_wait();
+    if (h < p.m) {
+      float* o = p.y + static_cast<int64_t>(t.urow + c0) * p.yp + h;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (c0 + j < t.rows) o[j * p.yp] = f(r[j]);
+    }
+  }
+}
+
+// da -> dgu, w a and this warp's 32 features' part of <da, a>; 16 rows at a time
+__device__ __forceinline__ void epi_dact(const ExGemmParams& p, const Tile& t, const EpiWarp& w, int part) {
+  const int tok = w.tid >> 4, chunk = w.tid & 15, ft = w.m0 + chunk * 8;
+  uint4 in[4];     // gate rows tok, tok + 8, then up rows
+  auto fetch = [&](int c0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = c0 + tok + 8 * (k & 1);
+      const __nv_bfloat16* q =
+          p.gu + static_cast<int64_t>(t.urow + row) * 2 * p.inner + (k >> 1) * p.inner + ft;
+      in[k] = load8(q, row < t.valid ? p.inner - ft : 0, p.gu_vec != 0);
+    }
+  };
+  int c0 = w.set * 16;
+  if (c0 < t.rows) fetch(c0);
+  for (; c0 < t.rows; c0 += 32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      sts16(staged(w.stg + (k >> 1) * 4096, tok + 8 * (k & 1), chunk, 256), in[k]);
+    if (c0 + 32 < t.rows) fetch(c0 + 32);
+    float wt[2][2], dot[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = c0 + 8 * i + 2 * (w.lane & 3) + j;
+        wt[i][j] = row < t.valid ? p.wr[t.prow + row] : 0.f;
+        dot[i][j] = 0.f;
+      }
+    w.bar();
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t r[8];
+      ptx::tmem_ld_16x256b_x2(w.taddr + (static_cast<uint32_t>(b * 16) << 16) + c0, r);
+      // matrix 2 i + c: rows 8 i.. of 8 features, chunk c of this 16-lane block
+      const int lr = (w.lane >> 4) * 8 + (w.lane & 7), lc = w.q4 * 4 + b * 2 + ((w.lane >> 3) & 1);
+      uint32_t g[4], u[4], a[4];
+      ptx::ldmatrix_x4_trans(staged(w.stg, lr, lc, 256), g);
+      ptx::ldmatrix_x4_trans(staged(w.stg + 4096, lr, lc, 256), u);
+      ptx::tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t gv = g[2 * i + c], uv = u[2 * i + c];
+          float dg[2], du[2], wa[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float gg = j ? hi_of(gv) : lo_of(gv), uu = j ? hi_of(uv) : lo_of(uv);
+            const float da = f(r[4 * i + 2 * c + j]);
+            const float s = sigmoid(gg), sl = gg * s;
+            dot[i][j] = fmaf(da, sl * uu, dot[i][j]);
+            const float wd = wt[i][j] * da;
+            dg[j] = wd * uu * (s * (1.f + gg * (1.f - s)));
+            du[j] = wd * sl;
+            wa[j] = wt[i][j] * (sl * uu);
+          }
+          g[2 * i + c] = pack(dg[0], dg[1]);
+          u[2 * i + c] = pack(du[0], du[1]);
+          a[2 * i + c] = pack(wa[0], wa[1]);
+        }
+      // a warp reads and writes its own four chunks only
+      ptx::stmatrix_x4_trans(staged(w.stg, lr, lc, 256), g);
+      ptx::stmatrix_x4_trans(staged(w.stg + 4096, lr, lc, 256), u);
+      ptx::stmatrix_x4_trans(staged(w.stg + 8192, lr, lc, 256), a);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(u[i], v[j], acc[i][j]);
+      for (int j = 0; j < 2; ++j) {
+        float v = dot[i][j];
+        v += __shfl_xor_sync(kFull, v, 4);
+        v += __shfl_xor_sync(kFull, v, 8);
+        v += __shfl_xor_sync(kFull, v, 16);
+        const int row = c0 + 8 * i + 2 * (w.lane & 3) + j;
+        if (w.lane < 4 && row < t.valid) p.part[(part + w.q4) * p.rows + t.urow + row] = v;
+      }
+    w.bar();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int row = tok + 8 * k;
+      if (c0 + row >= t.rows) continue;
+      const int64_t at = t.prow + c0 + row;
+      store8(p.dgu + at * 2 * p.ip + ft, lds16(staged(w.stg, row, chunk, 256)), p.ip - ft, true);
+      store8(p.dgu + at * 2 * p.ip + p.ip + ft, lds16(staged(w.stg + 4096, row, chunk, 256)), p.ip - ft, true);
+      store8(p.act + at * p.ip + ft, lds16(staged(w.stg + 8192, row, chunk, 256)), p.ip - ft, true);
+    }
+    w.bar();
+  }
+}
+
+// Weight gradients: lane = row, 128 bytes of columns at a time.
+template <int KIND>
+__device__ __forceinline__ void epi_dw(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
+  const bool f32 = p.dw_dt == kDtF32;
+  const int slab = f32 ? 32 : 64, per = f32 ? 4 : 8;   // columns per slab and 16-byte chunk
+  const int n0 = t.n * kExNTile;
+  const int row = w.q4 * 32 + w.lane;
+  for (int c0 = w.set * slab; c0 < kExNTile && n0 + c0 < p.n; c0 += 2 * slab) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h && f32) break;
+      uint32_t r[32];
+      if (t.kb > 0) {
+        ptx::tmem_ld_32x32b_x32(w.taddr + c0 + 32 * h, r);
+        ptx::tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) r[j] = 0u;
+      }
+      if (f32) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          sts16(staged(w.stg, row, c, 128), make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          sts16(staged(w.stg, row, 4 * h + c, 128),
+                make_uint4(pack(f(r[8 * c]), f(r[8 * c + 1])), pack(f(r[8 * c + 2]), f(r[8 * c + 3])),
+                           pack(f(r[8 * c + 4]), f(r[8 * c + 5])), pack(f(r[8 * c + 6]), f(r[8 * c + 7]))));
+      }
+    }
+    w.bar();
+    const int chunk = w.tid & 7, col = n0 + c0 + chunk * per;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int rr = (w.tid >> 3) + 16 * k;
+      int m = w.m0 + rr;
+      bool ok = m < p.m;
+      int64_t m_out = p.m;
+      if (KIND == kExDwIn) {     // [2][ip] rows -> [2][inner]
+        const int half = m >= p.ip;
+        m -= half * p.ip;
+        ok = ok && m < p.inner;
+        m += half * p.inner;
+        m_out = 2 * p.inner;
+      }
+      if (!ok || col >= p.n) continue;
+      const uint4 v = lds16(staged(w.stg, rr, chunk, 128));
+      const int64_t at = (t.e * m_out + m) * p.n + col;
+      if (!f32) {
+        store8(static_cast<__nv_bfloat16*>(p.dw) + at, v, p.n - col, p.dw_vec != 0);
+      } else {
+        float* o = static_cast<float*>(p.dw) + at;
+        if (p.dw_vec && p.n - col >= 4) {
+          *reinterpret_cast<uint4*>(o) = v;
+        } else {
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < p.n - col) o[j] = f(u[j]);
+        }
+      }
+    }
+    w.bar();
   }
 }
 
 }  // namespace
 
-// Row products.  blockIdx.y numbers row tiles of all experts, each expert's
-// rows starting a tile of its own.
-template <int MODE>
-__global__ void __launch_bounds__(kThreads) experts_rows_kernel(const __grid_constant__ ExpertsParams p) {
-  __shared__ float a[TK][TS + 4], b[TK][TS + 4];
-  __shared__ int s_e, s_r0, s_r1;
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ex_gemm_kernel(const __grid_constant__ ExGemmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sStage = smem;
+  uint8_t* sEpi = smem + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);   // CTA 0's count for both
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;     // [2] accumulator ready
+  uint64_t* tempty = tfull + 2;          // [2] accumulator drained by both CTAs (CTA 0's)
+  uint64_t* mma_drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* s_ok = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2 sets][2]
+  Scan scan;
+  scan.off = reinterpret_cast<int*>(smem + kScanOff);
+  scan.poff = scan.off + p.experts + 1;
+  scan.tt = scan.poff + p.experts + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int crank = static_cast<int>(ptx::cluster_ctarank());
+  const int tile0 = static_cast<int>(blockIdx.x >> 1), tstep = static_cast<int>(gridDim.x >> 1);
+
   if (threadIdx.x == 0) {
-    s_e = -1;
-    int left_tiles = blockIdx.y;
-    for (int e = 0; e < p.experts; ++e) {
-      const int r0 = row_begin(p, e), r1 = max(r0, row_begin(p, e + 1));
-      const int t = (r1 - r0 + TS - 1) / TS;
-      if (left_tiles < t) {
-        s_e = e;
-        s_r0 = r0 + left_tiles * TS;
-        s_r1 = min(s_r0 + TS, r1);
-        break;
-      }
-      left_tiles -= t;
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&tfull[b], 1);
+      ptx::mbar_init(&tempty[b], 16);    // the epilogue warps of both CTAs
+    }
+    ptx::mbar_init(mma_drain, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&p.mapA);
+    ptx::prefetch_tmap(&p.mapB);
   }
+  if (warp == 1) ptx::tmem_alloc_pair(tmem_slot, kTmemCols);
+  if (warp == 2) scan_offsets(scan, p.offsets, p.experts, p.rows, p.pad, KIND == kExDact, lane);
+  ptx::tc_fence_before();
   __syncthreads();
-  if (s_e < 0) return;
-  const int64_t N = MODE == kGu ? 2 * p.inner : MODE == kDa ? p.inner : p.hidden;
-  const int64_t K = MODE == kGu || MODE == kDa ? p.hidden : MODE == kDown ? p.inner : 2 * p.inner;
-  const int64_t n0 = blockIdx.x * static_cast<int64_t>(TS);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < K; k0 += TK) {
-    for (int i = threadIdx.x; i < TS * TK; i += kThreads) {
-      const int r = i / TK, k = i % TK;
-      const int64_t row = s_r0 + r;
-      const bool ok = row < s_r1 && k0 + k < K;
-      const int64_t tok = ok ? token_of(p, row) : -1;
-      a[k][r] = ok ? left<MODE>(p, row, k0 + k, tok) : 0.f;
-      // weights: neighbouring threads read neighbouring addresses
-      constexpr bool kn = MODE == kDa || MODE == kDx;
-      const int n = kn ? i % TS : i / TK, kk = kn ? i / TS : i % TK;
-      b[kk][n] = n0 + n < N && k0 + kk < K ? right<MODE>(p, s_e, n0 + n, k0 + kk) : 0.f;
-    }
-    __syncthreads();
-    fma_tile(a, b, acc, ty, tx);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t row = s_r0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (row >= s_r1 || n >= N) continue;
-      if (MODE == kDa) p.da[row * N + n] = acc[i][j];
-      else {
-        __nv_bfloat16* o = MODE == kGu ? p.gu : MODE == kDown ? p.y : p.dxr;
-        o[row * N + n] = __float2bfloat16_rn(acc[i][j]);
-      }
-    }
-}
+  ptx::cluster_sync();     // both CTAs' barriers are initialised
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int tiles = is_dw(KIND) ? p.experts * p.m_tiles * p.n_tiles : scan.tt[p.experts] * p.m_tiles;
 
-// Weight gradients: dw_in[e][f][h] = sum dgu[r][f] x[t][h],
-// dw_out[e][h][i] = sum dout[t][h] wact[r][i].
-template <int MODE>
-__global__ void __launch_bounds__(kThreads) experts_dw_kernel(const __grid_constant__ ExpertsParams p) {
-  __shared__ float a[TK][TS + 4], b[TK][TS + 4];
-  const int e = blockIdx.z;
-  const int64_t M = MODE == kDwIn ? 2 * p.inner : p.hidden, N = MODE == kDwIn ? p.hidden : p.inner;
-  const int64_t m0 = blockIdx.y * static_cast<int64_t>(TS), n0 = blockIdx.x * static_cast<int64_t>(TS);
-  const int r0 = row_begin(p, e), r1 = row_begin(p, e + 1);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int k0 = r0; k0 < r1; k0 += TK) {
-    for (int i = threadIdx.x; i < TS * TK; i += kThreads) {
-      const int c = i % TS, k = i / TS;
-      const int64_t row = k0 + k;
-      const int64_t tok = row < r1 ? token_of(p, row) : -1;
-      float u = 0.f, v = 0.f;
-      if (tok >= 0) {
-        if (m0 + c < M)
-          u = MODE == kDwIn ? bf(p.dgu, row * 2 * p.inner + m0 + c) : bf(p.dout, tok * p.dos + m0 + c);
-        if (n0 + c < N)
-          v = MODE == kDwIn ? bf(p.x, tok * p.xs + n0 + c) : bf(p.wact, row * p.inner + n0 + c);
-      }
-      a[k][c] = u;
-      b[k][c] = v;
-    }
-    __syncthreads();
-    fma_tile(a, b, acc, ty, tx);
-    __syncthreads();
-  }
-  void* o = MODE == kDwIn ? p.dw_in : p.dw_out;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m >= M || n >= N) continue;
-      const int64_t at = (e * M + m) * N + n;
-      if (p.dw_dt == kDtF32) static_cast<float*>(o)[at] = acc[i][j];
-      else static_cast<__nv_bfloat16*>(o)[at] = __float2bfloat16_rn(acc[i][j]);
-    }
-}
-
-// act = silu(g) u
-__global__ void __launch_bounds__(kThreads) experts_act_kernel(const __grid_constant__ ExpertsParams p) {
-  const int64_t rows = row_begin(p, p.experts);
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
-    for (int64_t i = threadIdx.x; i < p.inner; i += kThreads) {
-      float slope;
-      const float g = bf(p.gu, row * 2 * p.inner + i), u = bf(p.gu, row * 2 * p.inner + p.inner + i);
-      p.act[row * p.inner + i] = __float2bfloat16_rn(silu_parts(g, &slope) * u);
-    }
-}
-
-// dgu, w a and dweights of one row per block turn
-__global__ void __launch_bounds__(kThreads) experts_dact_kernel(const __grid_constant__ ExpertsParams p) {
-  __shared__ float s_part[kThreads / 32];
-  const int64_t rows = row_begin(p, p.experts);
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int32_t s = p.src[row];
-    const bool ok = s >= 0 && s < p.rows;
-    const float w = ok ? p.weights[s] : 0.f;
-    float dot = 0.f;
-    for (int64_t i = threadIdx.x; i < p.inner; i += kThreads) {
-      float slope;
-      const float g = bf(p.gu_in, row * 2 * p.inner + i), u = bf(p.gu_in, row * 2 * p.inner + p.inner + i);
-      const float sl = silu_parts(g, &slope), da = p.da[row * p.inner + i];
-      dot = fmaf(da, sl * u, dot);
-      p.dgu[row * 2 * p.inner + i] = __float2bfloat16_rn(w * da * u * slope);
-      p.dgu[row * 2 * p.inner + p.inner + i] = __float2bfloat16_rn(w * da * sl);
-      p.wact[row * p.inner + i] = __float2bfloat16_rn(w * sl * u);
-    }
+  if (warp == 0) {
+    // ---- TMA producer -------------------------------------------------------------------
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool stop = false;
+      for (int tile = tile0; tile < tiles && !stop; tile += tstep) {
+        const Tile t = decode<KIND>(p, scan, tile);
+        const int half = t.cols / 2, boxes = (half + 31) / 32;
+        const uint32_t bytes = is_dw(KIND) ? 2 * kStageBytes : 2 * (kOpBytes + boxes * 4096);
+        const int m0 = t.m * kExMTile + crank * 128;
+        for (int i = 0; i < t.kb; ++i) {
+          if (!wait_bounded(&empty[stage], phase ^ 1, abort_flag, p.status, p.timeout_ns, true)) {
+            stop = true;
+            break;
+          }
+          if (crank == 0) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
+          const uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&full[stage]), 0);
+          uint8_t* a = sStage + stage * kStageBytes;
+          uint8_t* b = a + kOpBytes;
+          const int k = i * BK;
+          if (KIND == kExUp) {
+            // 8 features x (gate, up) x 8 groups: 128 rows
+            ptx::tma_load_5d_pair(a, &p.mapA, bar, k, 0, 0, m0 >> 4, t.e);
+          } else if (KIND == kExDown) {
+            ptx::tma_load_3d_pair(a, &p.mapA, bar, k, m0, t.e);
+          } else if (is_dw(KIND)) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0 && ok && p.dweights) {
-      for (int k = 1; k < kThreads / 32; ++k) dot += s_part[k];
-      p.dweights[s] = dot;
+            for (int h = 0; h < 2; ++h)
+              ptx::tma_load_2d_pair(a + h * 8192, &p.mapA, bar, m0 + 64 * h, t.prow + k);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              ptx::tma_load_3d_pair(a + h * 8192, &p.mapA, bar, m0 + 64 * h, k, t.e);
+          }
+          if (is_dw(KIND)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              ptx::tma_load_2d_pair(b + h * 8192, &p.mapB, bar, t.n * kExNTile + crank * 128 + 64 * h,
+                                    t.prow + k);
+          } else {
+            for (int h = 0; h < boxes; ++h)
+              ptx::tma_load_2d_pair(b + h * 4096, &p.mapB, bar, k, t.prow + crank * half + 32 * h);
+          }
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // CTA 0: the last copies of both CTAs have landed before the pair exits
+      if (crank == 0)
+        for (int j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
+          wait_bounded(&full[j % kStages], (j / kStages) & 1, abort_flag, p.status, p.timeout_ns, false);
     }
-    __syncthreads();
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- MMA issuer (CTA 0) --------------------------------------------------------------
+    if (lane == 0 && crank == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0;
+      bool stop = false;
+      for (int tile = tile0; tile < tiles && !stop; tile += tstep) {
+        const Tile t = decode<KIND>(p, scan, tile);
+        if (t.kb == 0) continue;
+        const uint32_t idesc = ptx::idesc_bf16_f32(kExMTile, t.cols) | (a_mn(KIND) ? 1u << 15 : 0u) |
+                               (is_dw(KIND) ? 1u << 16 : 0u);
+        const int buf = acc & 1;
+        if (!wait_bounded(&tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag, p.status, p.timeout_ns, true))
+          break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + buf * 256;
+        for (int i = 0; i < t.kb; ++i) {
+          if (!wait_bounded(&full[stage], phase, abort_flag, p.status, p.timeout_ns, true)) {
+            stop = true;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t a0 = ptx::smem_u32(sStage + stage * kStageBytes), b0 = a0 + kOpBytes;
+#pragma unroll
+          for (int k = 0; k < BK / UMMA_K; ++k) {
+            // K-major: along the 128-byte row; MN-major: 16 rows (two 1024-byte atoms)
+            const uint64_t da = a_mn(KIND) ? ptx::sdesc_mnmajor_sw128(a0 + k * 2048, 8192, 1024)
+                                           : ptx::sdesc_kmajor_sw128(a0 + k * UMMA_K * 2);
+            const uint64_t db = is_dw(KIND) ? ptx::sdesc_mnmajor_sw128(b0 + k * 2048, 8192, 1024)
+                                            : ptx::sdesc_kmajor_sw128(b0 + k * UMMA_K * 2);
+            ptx::umma_bf16_pair(d, da, db, idesc, (i > 0 || k > 0) ? 1u : 0u);
+          }
+          ptx::umma_commit_pair(&empty[stage], 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        ptx::umma_commit_pair(&tfull[buf], 0x3);
+        ++acc;
+      }
+      // no MMA may still run when TMEM is freed
+      ptx::umma_commit_pair(mma_drain, 0x1);
+      wait_bounded(mma_drain, 0, abort_flag, p.status, p.timeout_ns, false);
+    }
+    __syncwarp();
+  } else {
+    // ---- epilogue --------------------------------------------------------------------------
+    EpiWarp w;
+    w.q4 = warp & 3;       // TMEM lane quadrant this warp may read
+    w.set = (warp - 2) >> 2;
+    w.lane = lane;
+    w.tid = ((warp - 2) & 3) * 32 + lane;
+    w.stg = ptx::smem_u32(sEpi + w.set * kSetBytes);
+    int acc = 0;
+    for (int tile = tile0, it = 0; tile < tiles; tile += tstep, ++it) {
+      const Tile t = decode<KIND>(p, scan, tile);
+      w.m0 = t.m * kExMTile + crank * 128;
+      const int buf = acc & 1;
+      w.taddr = tmem + buf * 256 + (static_cast<uint32_t>(w.q4 * 32) << 16);
+      if (t.kb > 0) {
+        wait_bounded(&tfull[buf], (acc >> 1) & 1, abort_flag, p.status, p.timeout_ns, false);
+        // one decision for the set (its warps share a barrier); the slot
+        // alternates, so it is rewritten only after everyone has read it
+        if (w.tid == 0) s_ok[2 * w.set + (it & 1)] = !*abort_flag;
+        w.bar();
+        if (!s_ok[2 * w.set + (it & 1)]) break;
+        ptx::tc_fence_after();
+      }
+      if (KIND == kExUp) epi_up(p, t, w);
+      else if (KIND == kExDact) epi_dact(p, t, w, (t.m * 2 + crank) * 4);
+      else if (is_dw(KIND)) epi_dw<KIND>(p, t, w);
+      else epi_rows(p, t, w);
+      if (t.kb > 0) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), 0));
+        ++acc;
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();     // no copy, MMA or arrival still aims at the partner
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// Copies the rows of x (and dout) into expert order, a warp per row; HBM-bound.
+__global__ void __launch_bounds__(256) ex_gather_kernel(const __grid_constant__ ExGatherParams p) {
+  extern __shared__ int s_scan[];
+  Scan s;
+  s.off = s_scan;
+  s.poff = s.off + p.experts + 1;
+  s.tt = s.poff + p.experts + 1;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) scan_offsets(s, p.offsets, p.experts, p.rows, p.pad, false, lane);
+  __syncthreads();
+  const int total = s.poff[p.experts];
+  for (int64_t r = blockIdx.x * 8LL + (threadIdx.x >> 5); r < total; r += gridDim.x * 8LL) {
+    const int e = find(s.poff, p.experts, static_cast<int>(r));
+    const int urow = s.off[e] + static_cast<int>(r) - s.poff[e];
+    int32_t sv = urow < s.off[e + 1] ? p.src[urow] : -1;
+    if (sv >= p.rows) sv = -1;
+    const int64_t tok = sv < 0 ? 0 : sv / p.top_k;
+    if (p.wr && lane == 0) p.wr[r] = sv < 0 ? 0.f : p.weights[sv];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (!p.x[q]) continue;
+      const __nv_bfloat16* in = p.x[q] + tok * p.xs[q];
+      __nv_bfloat16* out = p.out[q] + r * p.hp;
+      for (int64_t c = lane * 8; c < p.hp; c += 256) {
+        const int n = sv < 0 ? 0 : static_cast<int>(min(p.hidden - c, static_cast<int64_t>(8)));
+        *reinterpret_cast<uint4*>(out + c) = load8(in + c, n, p.vec != 0);
+      }
+    }
   }
 }
 
-// out[t] = sum over slots, in slot order
-template <bool WEIGHTED>
-__global__ void __launch_bounds__(kThreads)
-    experts_combine_kernel(const __grid_constant__ ExpertsParams p, const __nv_bfloat16* rows,
-                           __nv_bfloat16* out, int64_t outs) {
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x)
-    for (int64_t h = threadIdx.x; h < p.hidden; h += kThreads) {
-      float v = 0.f;
-      for (int j = 0; j < p.top_k; ++j) {
-        const int32_t r = p.pos[t * p.top_k + j];
-        if (r < 0 || r >= p.rows) continue;
-        v = fmaf(WEIGHTED ? p.weights[t * p.top_k + j] : 1.f, bf(rows, r * p.hidden + h), v);
+// out[t] = sum over slots, in slot order, four columns a thread; HBM-bound.
+__global__ void __launch_bounds__(256) ex_combine_kernel(const __grid_constant__ ExCombineParams p) {
+  const int64_t quads = (p.hidden + 3) / 4;
+  const int64_t n = p.tokens * quads;
+  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+    const int64_t t = i / quads, c = (i - t * quads) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < p.top_k; j0 += 8) {
+      float4 y[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int32_t r = j0 + j < p.top_k ? p.pos[t * p.top_k + j0 + j] : -1;
+        const bool ok = r >= 0 && r < p.rows;
+        w[j] = !ok ? 0.f : p.weights ? p.weights[t * p.top_k + j0 + j] : 1.f;
+        y[j] = ok ? *reinterpret_cast<const float4*>(p.y + r * p.yp + c) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      out[t * outs + h] = __float2bfloat16_rn(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v.x = fmaf(w[j], y[j].x, v.x);
+        v.y = fmaf(w[j], y[j].y, v.y);
+        v.z = fmaf(w[j], y[j].z, v.z);
+        v.w = fmaf(w[j], y[j].w, v.w);
+      }
     }
+    __nv_bfloat16* o = p.out + t * p.outs + c;
+    if (p.vec && c + 4 <= p.hidden) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack(v.x, v.y), pack(v.z, v.w));
+    } else {
+      const float u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < p.hidden) o[j] = __float2bfloat16_rn(u[j]);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) ex_dweights_kernel(const __grid_constant__ ExWeightParams p) {
+  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < p.rows; i += gridDim.x * 256LL) {
+    const int32_t r = p.pos[i];
+    float v = 0.f;
+    if (r >= 0 && r < p.rows)
+      for (int k = 0; k < p.parts; ++k) v += p.part[k * p.rows + r];
+    p.dweights[i] = v;
+  }
+}
+
+__global__ void __launch_bounds__(256)
+    ex_repack_kernel(const __nv_bfloat16* in, int64_t mats, int64_t rows, int64_t cols, __nv_bfloat16* out,
+                     int64_t rows_p, int64_t cols_p) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t r = blockIdx.x * 8LL + (threadIdx.x >> 5); r < mats * rows_p; r += gridDim.x * 8LL) {
+    const int64_t m = r / rows_p, rr = r - m * rows_p;
+    const __nv_bfloat16* q = in + (m * rows + min(rr, rows - 1)) * cols;
+    for (int64_t c = lane * 8; c < cols_p; c += 256) {
+      const int n = rr < rows ? static_cast<int>(min(cols - c, static_cast<int64_t>(8))) : 0;
+      *reinterpret_cast<uint4*>(out + r * cols_p + c) = load8(q + c, n, false);
+    }
+  }
 }
 
 namespace {
 
-template <int MODE>
-cudaError_t rows_launch(const ExpertsParams& p, int64_t n, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((n + TS - 1) / TS),
-                  static_cast<unsigned>((p.rows + TS - 1) / TS + p.experts));
-  experts_rows_kernel<MODE><<<grid, kThreads, 0, s>>>(p);
+template <int KIND>
+cudaError_t gemm_launch(const ExGemmParams& p, int sms, cudaStream_t s) {
+  const int smem = gemm_smem(p.experts);
+  const cudaError_t e = cudaFuncSetAttribute(ex_gemm_kernel<KIND>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  ex_gemm_kernel<KIND><<<sms / 2 * 2, kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
-unsigned many(int64_t n) { return static_cast<unsigned>(n < 4096 ? n : 4096); }
+unsigned some(int64_t n, int64_t most) { return static_cast<unsigned>(std::min(std::max<int64_t>(n, 1), most)); }
 
 }  // namespace
 
-cudaError_t launch_experts_gu(const ExpertsParams& p, cudaStream_t s) { return rows_launch<kGu>(p, 2 * p.inner, s); }
-cudaError_t launch_experts_down(const ExpertsParams& p, cudaStream_t s) { return rows_launch<kDown>(p, p.hidden, s); }
-cudaError_t launch_experts_da(const ExpertsParams& p, cudaStream_t s) { return rows_launch<kDa>(p, p.inner, s); }
-cudaError_t launch_experts_dx(const ExpertsParams& p, cudaStream_t s) { return rows_launch<kDx>(p, p.hidden, s); }
+cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, cudaStream_t s) {
+  switch (kind) {
+    case kExUp: return gemm_launch<kExUp>(p, sms, s);
+    case kExDown: return gemm_launch<kExDown>(p, sms, s);
+    case kExDact: return gemm_launch<kExDact>(p, sms, s);
+    case kExDx: return gemm_launch<kExDx>(p, sms, s);
+    case kExDwIn: return gemm_launch<kExDwIn>(p, sms, s);
+    default: return gemm_launch<kExDwOut>(p, sms, s);
+  }
+}
 
-cudaError_t launch_experts_act(const ExpertsParams& p, cudaStream_t s) {
-  experts_act_kernel<<<many(p.rows), kThreads, 0, s>>>(p);
+cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, cudaStream_t s) {
+  ex_gather_kernel<<<some((padded_rows + 7) / 8, 2432), 256, 3 * (p.experts + 1) * sizeof(int), s>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_experts_dact(const ExpertsParams& p, cudaStream_t s) {
-  experts_dact_kernel<<<many(p.rows), kThreads, 0, s>>>(p);
+cudaError_t launch_ex_combine(const ExCombineParams& p, cudaStream_t s) {
+  ex_combine_kernel<<<some((p.tokens * ((p.hidden + 3) / 4) + 255) / 256, 1 << 20), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_experts_dw(const ExpertsParams& p, bool w_out, cudaStream_t s) {
-  const int64_t M = w_out ? p.hidden : 2 * p.inner, N = w_out ? p.inner : p.hidden;
-  const dim3 grid(static_cast<unsigned>((N + TS - 1) / TS), static_cast<unsigned>((M + TS - 1) / TS),
-                  static_cast<unsigned>(p.experts));
-  if (w_out) experts_dw_kernel<kDwOut><<<grid, kThreads, 0, s>>>(p);
-  else experts_dw_kernel<kDwIn><<<grid, kThreads, 0, s>>>(p);
+cudaError_t launch_ex_dweights(const ExWeightParams& p, cudaStream_t s) {
+  ex_dweights_kernel<<<some((p.rows + 255) / 256, 1 << 16), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_experts_combine(const ExpertsParams& p, const __nv_bfloat16* rows, bool weighted,
-                                   __nv_bfloat16* out, int64_t outs, cudaStream_t s) {
-  if (weighted) experts_combine_kernel<true><<<many(p.tokens), kThreads, 0, s>>>(p, rows, out, outs);
-  else experts_combine_kernel<false><<<many(p.tokens), kThreads, 0, s>>>(p, rows, out, outs);
+cudaError_t launch_ex_repack(const __nv_bfloat16* in, int64_t mats, int64_t rows, int64_t cols,
+                             __nv_bfloat16* out, int64_t rows_p, int64_t cols_p, cudaStream_t s) {
+  ex_repack_kernel<<<some((mats * rows_p + 7) / 8, 1 << 14), 256, 0, s>>>(in, mats, rows, cols, out, rows_p,
+                                                                         cols_p);
   return cudaGetLastError();
 }
 
