@@ -223,8 +223,10 @@ def _dtype_code(t) -> int:
 
 def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
+        # the handle alone: torch.cuda.current_stream() builds a Stream object,
+        # several microseconds of a small call
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -448,36 +450,36 @@ def muon_assign_owners(costs, n_ranks: int, nbytes=None, elems=None, layers=None
 
 
 # ---- the mixture-of-experts block ------------------------------------------------------
-def _codes():
-    import torch
-    return {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16, torch.float8_e4m3fn: MUON_E4M3}
-
-
-_DTYPE_CODES = None
+_DTYPE_CODES = {}
 
 
 def _code(dtype) -> int:
-    global _DTYPE_CODES
-    if _DTYPE_CODES is None:
-        _DTYPE_CODES = _codes()
-    try:
-        return _DTYPE_CODES[dtype]
-    except KeyError:
-        raise TypeError(f"unsupported dtype {dtype}") from None
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        import torch
+        _DTYPE_CODES.update({torch.float32: MUON_F32, torch.bfloat16: MUON_BF16,
+                             torch.float8_e4m3fn: MUON_E4M3})
+        code = _DTYPE_CODES.get(dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def _rows(t, name: str, cols: Optional[int] = None, rows: Optional[int] = None):
-    """(pointer, row stride, dtype code) of a CUDA tensor [..., cols] whose
-    leading dimensions are one run of rows."""
-    if t.dim() != 2:
+    """(pointer, row stride, dtype code) of a CUDA tensor [rows, cols] whose
+    columns are adjacent in memory."""
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be [rows, cols]")
-    r, c = t.shape
+    r, c = shape
     if (cols is not None and c != cols) or (rows is not None and r != rows):
-        raise ValueError(f"{name} is {tuple(t.shape)}, expected {(rows, cols)}")
-    if c > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: neighbouring columns must be adjacent in memory")
+        raise ValueError(f"{name} is {tuple(shape)}, expected {(rows, cols)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.is_contiguous():
+        return t.data_ptr(), c, _code(t.dtype)
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: neighbouring columns must be adjacent in memory")
     stride = t.stride(0) if r > 1 else c
     if r > 1 and stride < c:
         raise ValueError(f"{name}: rows overlap")
@@ -486,7 +488,7 @@ def _rows(t, name: str, cols: Optional[int] = None, rows: Optional[int] = None):
 
 def _dense(t, name: str, shape, dtype) -> int:
     """Pointer of a contiguous CUDA tensor of exactly this shape and dtype."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
@@ -502,30 +504,31 @@ def muon_rmsnorm_forward(x, gain=None, residual=None, eps: float = 1e-6, y_dtype
     is None without a residual unless given.  Outputs that are not given are
     allocated; h may be `residual` itself."""
     import torch
+    xp, xs, xc = _rows(x, "x")
     rows, cols = x.shape
-    a = RmsNorm(rows=rows, cols=cols, eps=eps, group=group)
-    a.x, a.x_stride, a.x_dtype = _rows(x, "x")
+    rp, rs, rc, gp, gc, hp, hs, hc, sp = None, 0, 0, None, 0, None, 0, 0, None
     if residual is not None:
-        a.residual, a.residual_stride, a.residual_dtype = _rows(residual, "residual", cols, rows)
+        rp, rs, rc = _rows(residual, "residual", cols, rows)
         if h is None:
-            h = torch.empty((rows, cols), dtype=residual.dtype, device=x.device)
+            h = residual.new_empty((rows, cols))
     if gain is not None:
-        a.gain, a.gain_dtype = _dense(gain, "gain", (cols,), gain.dtype), _code(gain.dtype)
+        gp, gc = _dense(gain, "gain", (cols,), gain.dtype), _code(gain.dtype)
     if h is not None:
-        a.h, a.h_stride, a.h_dtype = _rows(h, "h", cols, rows)
+        hp, hs, hc = _rows(h, "h", cols, rows)
     if y is None:
-        y = torch.empty((rows, cols), dtype=y_dtype or x.dtype, device=x.device)
+        y = x.new_empty((rows, cols), dtype=y_dtype)
     elif y_dtype is not None and y.dtype != y_dtype:
         raise ValueError(f"y is {y.dtype}, expected {y_dtype}")
-    a.y, a.y_stride, a.y_dtype = _rows(y, "y", cols, rows)
-    if a.y_dtype == MUON_E4M3:
+    yp, ys, yc = _rows(y, "y", cols, rows)
+    if yc == MUON_E4M3:
         n = -(-cols // group) if group > 0 else 1
         if scales is None:
-            scales = torch.empty((rows, n), dtype=torch.float32, device=x.device)
-        a.scales = _dense(scales, "scales", (rows, n), torch.float32)
+            scales = x.new_empty((rows, n), dtype=torch.float32)
+        sp = _dense(scales, "scales", (rows, n), torch.float32)
     else:
         scales = None
-    check(load().muon_rmsnorm_forward(ctypes.byref(a), _stream_ptr(stream)), "muon_rmsnorm_forward")
+    a = RmsNorm(rows, cols, xp, xs, rp, rs, gp, hp, hs, yp, ys, sp, xc, rc, gc, hc, yc, group, eps)
+    check(load().muon_rmsnorm_forward(a, _stream_ptr(stream)), "muon_rmsnorm_forward")
     return y, h, scales
 
 
@@ -536,22 +539,23 @@ def muon_rmsnorm_backward(dy, h, gain=None, dres=None, eps: float = 1e-6, dh=Non
     h along the residual stream, added; dgain is f32 [cols] (None when not
     wanted)."""
     import torch
+    dp, ds, dc = _rows(dy, "dy")
     rows, cols = dy.shape
-    a = RmsNormGrad(rows=rows, cols=cols, eps=eps)
-    a.dy, a.dy_stride, a.dy_dtype = _rows(dy, "dy")
-    a.h, a.h_stride, a.h_dtype = _rows(h, "h", cols, rows)
+    hp, hs, hc = _rows(h, "h", cols, rows)
+    gp, gc, rp, rs, rc, wp = None, 0, None, 0, 0, None
     if gain is not None:
-        a.gain, a.gain_dtype = _dense(gain, "gain", (cols,), gain.dtype), _code(gain.dtype)
+        gp, gc = _dense(gain, "gain", (cols,), gain.dtype), _code(gain.dtype)
     if dres is not None:
-        a.dres, a.dres_stride, a.dres_dtype = _rows(dres, "dres", cols, rows)
+        rp, rs, rc = _rows(dres, "dres", cols, rows)
     if dh is None:
-        dh = torch.empty((rows, cols), dtype=h.dtype, device=dy.device)
-    a.dh, a.dh_stride, a.dh_dtype = _rows(dh, "dh", cols, rows)
+        dh = h.new_empty((rows, cols))
+    op, os_, oc = _rows(dh, "dh", cols, rows)
     if dgain is None and want_dgain:
-        dgain = torch.empty(cols, dtype=torch.float32, device=dy.device)
+        dgain = dy.new_empty(cols, dtype=torch.float32)
     if dgain is not None:
-        a.dgain = _dense(dgain, "dgain", (cols,), torch.float32)
-    check(load().muon_rmsnorm_backward(ctypes.byref(a), _stream_ptr(stream)), "muon_rmsnorm_backward")
+        wp = _dense(dgain, "dgain", (cols,), torch.float32)
+    a = RmsNormGrad(rows, cols, dp, ds, hp, hs, gp, rp, rs, op, os_, wp, dc, hc, gc, rc, oc, eps)
+    check(load().muon_rmsnorm_backward(a, _stream_ptr(stream)), "muon_rmsnorm_backward")
     return dh, dgain
 
 
@@ -563,11 +567,11 @@ def make_route_config(experts: int, top_k: int, score: int = ROUTE_SOFTMAX, grou
                        group_score, int(renormalize), scale)
 
 
-def _plan_tensors(tokens: int, top_k: int, experts: int, device):
+def _plan_tensors(like, tokens: int, top_k: int, experts: int):
     import torch
-    return (torch.empty(experts + 1, dtype=torch.int32, device=device),
-            torch.empty(tokens * top_k, dtype=torch.int32, device=device),
-            torch.empty((tokens, top_k), dtype=torch.int32, device=device))
+    return (like.new_empty(experts + 1, dtype=torch.int32),
+            like.new_empty(tokens * top_k, dtype=torch.int32),
+            like.new_empty((tokens, top_k), dtype=torch.int32))
 
 
 def muon_route_forward(logits, cfg: RouteConfig, bias=None, mask=None, plan: bool = True,
@@ -578,20 +582,20 @@ def muon_route_forward(logits, cfg: RouteConfig, bias=None, mask=None, plan: boo
     [tokens], tokens to leave out are false."""
     import torch
     ptr, stride, code = _rows(logits, "logits", cfg.experts)
-    tokens, dev = logits.shape[0], logits.device
-    idx = torch.empty((tokens, cfg.top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((tokens, cfg.top_k), dtype=torch.float32, device=dev)
-    off = src = pos = None
+    tokens, k = logits.shape[0], cfg.top_k
+    idx = logits.new_empty((tokens, k), dtype=torch.int32)
+    weights = logits.new_empty((tokens, k), dtype=torch.float32)
+    off = src = pos = op = sp = pp = None
     if plan:
-        off, src, pos = _plan_tensors(tokens, cfg.top_k, cfg.experts, dev)
+        off, src, pos = _plan_tensors(logits, tokens, k, cfg.experts)
+        op, sp, pp = off.data_ptr(), src.data_ptr(), pos.data_ptr()
     b = _dense(bias, "bias", (cfg.experts,), torch.float32) if bias is not None else None
     m = None
     if mask is not None:
         m = _dense(mask, "mask", (tokens,), torch.bool if mask.dtype == torch.bool else torch.uint8)
-    check(load().muon_route_forward(
-        ctypes.byref(cfg), ptr, code, stride, tokens, b, m, idx.data_ptr(), weights.data_ptr(),
-        off.data_ptr() if plan else None, src.data_ptr() if plan else None,
-        pos.data_ptr() if plan else None, _stream_ptr(stream)), "muon_route_forward")
+    check(load().muon_route_forward(cfg, ptr, code, stride, tokens, b, m, idx.data_ptr(),
+                                    weights.data_ptr(), op, sp, pp, _stream_ptr(stream)),
+          "muon_route_forward")
     return Route(idx, weights, off, src, pos)
 
 
@@ -600,7 +604,7 @@ def muon_route_plan(idx, experts: int, stream=None):
     import torch
     tokens, top_k = idx.shape
     p = _dense(idx, "idx", (tokens, top_k), torch.int32)
-    off, src, pos = _plan_tensors(tokens, top_k, experts, idx.device)
+    off, src, pos = _plan_tensors(idx, tokens, top_k, experts)
     check(load().muon_route_plan(p, tokens, top_k, experts, off.data_ptr(), src.data_ptr(),
                                  pos.data_ptr(), _stream_ptr(stream)), "muon_route_plan")
     return off, src, pos
@@ -612,13 +616,13 @@ def muon_route_backward(logits, cfg: RouteConfig, idx, dweights, dlogits=None, s
     ptr, stride, code = _rows(logits, "logits", cfg.experts)
     tokens = logits.shape[0]
     if dlogits is None:
-        dlogits = torch.empty((tokens, cfg.experts), dtype=logits.dtype, device=logits.device)
+        dlogits = logits.new_empty((tokens, cfg.experts))
     dptr, dstride, dcode = _rows(dlogits, "dlogits", cfg.experts, tokens)
     if dcode != code:
         raise ValueError("dlogits must have the logits' dtype")
     i = _dense(idx, "idx", (tokens, cfg.top_k), torch.int32)
     w = _dense(dweights, "dweights", (tokens, cfg.top_k), torch.float32)
-    check(load().muon_route_backward(ctypes.byref(cfg), ptr, code, stride, tokens, i, w, dptr, dstride,
+    check(load().muon_route_backward(cfg, ptr, code, stride, tokens, i, w, dptr, dstride,
                                      _stream_ptr(stream)), "muon_route_backward")
     return dlogits
 
@@ -653,14 +657,14 @@ def muon_experts_forward(x, w_in, w_out, route: Route, save: bool = False, out=N
     import torch
     a = _experts_args(x, w_in, w_out, route)
     if out is None:
-        out = torch.empty((a.tokens, a.hidden), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((a.tokens, a.hidden))
     elif out.dtype != torch.bfloat16:
         raise TypeError(f"out must be bfloat16, got {out.dtype}")
     optr, ostride, _ = _rows(out, "out", a.hidden, a.tokens)
     gu = None
     if save:
-        gu = torch.empty((a.tokens * a.top_k, 2 * a.inner), dtype=torch.bfloat16, device=x.device)
-    check(load().muon_experts_forward(ctypes.byref(a), optr, ostride,
+        gu = x.new_empty((a.tokens * a.top_k, 2 * a.inner))
+    check(load().muon_experts_forward(a, optr, ostride,
                                       gu.data_ptr() if save else None, _stream_ptr(stream)),
           "muon_experts_forward")
     return out, gu
@@ -681,19 +685,19 @@ def muon_experts_backward(dout, x, w_in, w_out, route: Route, gu, dw_dtype=None,
     g = _dense(gu, "gu", (a.tokens * a.top_k, 2 * a.inner), bf16)
     xptr, xstride = None, a.hidden
     if dx is None and want_dx:
-        dx = torch.empty((a.tokens, a.hidden), dtype=bf16, device=x.device)
+        dx = x.new_empty((a.tokens, a.hidden))
     if dx is not None:
         xptr, xstride, _ = _rows(dx, "dx", a.hidden, a.tokens)
     if want_dw:
         dw_dtype = dw_dtype or (dw_in.dtype if dw_in is not None else torch.float32)
         if dw_in is None:
-            dw_in = torch.empty(w_in.shape, dtype=dw_dtype, device=x.device)
+            dw_in = w_in.new_empty(w_in.shape, dtype=dw_dtype)
         if dw_out is None:
-            dw_out = torch.empty(w_out.shape, dtype=dw_dtype, device=x.device)
+            dw_out = w_out.new_empty(w_out.shape, dtype=dw_dtype)
     code = _code(dw_dtype) if dw_dtype is not None else MUON_F32
-    dweights = torch.empty((a.tokens, a.top_k), dtype=torch.float32, device=x.device)
+    dweights = x.new_empty((a.tokens, a.top_k), dtype=torch.float32)
     check(load().muon_experts_backward(
-        ctypes.byref(a), dptr, dstride, g, xptr, xstride,
+        a, dptr, dstride, g, xptr, xstride,
         _dense(dw_in, "dw_in", w_in.shape, dw_dtype) if want_dw else None,
         _dense(dw_out, "dw_out", w_out.shape, dw_dtype) if want_dw else None,
         code, dweights.data_ptr(), _stream_ptr(stream)), "muon_experts_backward")

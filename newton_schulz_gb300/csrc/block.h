@@ -58,6 +58,8 @@ struct NormGradParams {
   int dy_dt, h_dt, g_dt, dr_dt, dh_dt;
   int vec;
   float eps;
+  unsigned* status;
+  unsigned long long timeout_ns;
 };
 
 cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t s);
@@ -126,6 +128,7 @@ constexpr int kExNTile = 256;     // most token rows (gradients: columns) per CT
 
 struct ExGemmParams {
   CUtensorMap mapA, mapB;         // weight-side and token-side operand
+  CUtensorMap mapB32;             // token rows in boxes of 32 (kExDw*: unused)
   const int32_t* offsets;         // [experts + 1]
   int64_t rows;                   // tokens * top_k, the most rows there are
   int experts;
@@ -134,16 +137,19 @@ struct ExGemmParams {
   int kb;                         // K blocks of 64 (kExDw*: from the expert's rows)
   int m, n;                       // valid M (padded for kExDwIn) and, kExDw*, N
   int inner, ip;                  // inner, and rounded up to 8
-  __nv_bfloat16* act;             // [padded rows][ip]: kExUp act, kExDact w a
+  int ap, gp;                     // pitches of act and dgu
+  __nv_bfloat16* act;             // [padded rows][ap]: kExUp act, kExDact w a
   __nv_bfloat16* gu;              // [rows][2 inner]: kExUp output or null, kExDact input
   int gu_vec;                     // 16-byte accesses to gu are legal
   float* y;                       // [rows][yp]
   int64_t yp;
   const float* wr;                // [padded rows] weight of a row
-  __nv_bfloat16* dgu;             // [padded rows][2 ip]
+  __nv_bfloat16* dgu;             // [padded rows][gp], gate part then up part at ip
   float* part;                    // [m_tiles * 8][rows] parts of dweights
   void* dw;
   int dw_dt, dw_vec;
+  int stages;                     // ring depth (set at the launch)
+  int a_whole;                    // MN-major weights in one copy of two 64-column chunks
   unsigned* status;
   unsigned long long timeout_ns;
 };

@@ -152,6 +152,7 @@ muon_status_t norm_grad_impl(const muon_rmsnorm_grad_t* a, cudaStream_t stream) 
   ApiDevice d;
   MUON_TRY(device(&d));
   Counter c;
+  p.status = d.status, p.timeout_ns = d.timeout_ns;
   const int slots = norm_grad_slots(p, d.sms);
   if (a->dgain) {
     char* ws = nullptr;
@@ -406,6 +407,25 @@ bool map2(CUtensorMap* m, const void* base, int64_t d0, int64_t d1, int64_t pitc
   const uint32_t box[2] = {64, b1};
   return encode_bf16_nd(m, base, 2, dims, st, box);
 }
+// Token rows, in boxes of 128 and of 32.
+bool map_rows(ExGemmParams* p, const void* base, int64_t d0, int64_t rows, int64_t pitch) {
+  return map2(&p->mapB, base, d0, rows, pitch, 128) && map2(&p->mapB32, base, d0, rows, pitch, 32);
+}
+// A matrix read MN-major in one copy: columns as chunks of 64, box 64 x 64 x 2.
+// `cols` is a multiple of 64; rows of d2 matrices.
+bool map_mn(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t pitch, int64_t d2) {
+  const uint64_t dims[4] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols / 64),
+                            static_cast<uint64_t>(d2)};
+  const uint64_t st[3] = {static_cast<uint64_t>(pitch * 2), 128, static_cast<uint64_t>(pitch * rows * 2)};
+  const uint32_t box[4] = {64, 64, 2, 1};
+  return encode_bf16_nd(m, base, d2 ? 4 : 3, dims, st, box);
+}
+// MN-major weights [e][rows][cols]: in one copy where the columns are whole chunks.
+bool map_weights_mn(ExGemmParams* p, const void* base, int64_t cols, int64_t rows, int64_t pitch) {
+  p->a_whole = cols % 64 == 0;
+  return p->a_whole ? map_mn(&p->mapA, base, cols, rows, pitch, p->experts)
+                    : map3(&p->mapA, base, cols, rows, p->experts, pitch, 64);
+}
 // W_in as [e][ip / 8][gate, up][8][hidden]: a box of 64 x 8 x 2 x 8 is 128
 // rows, 8 gate rows and 8 up rows in turn.
 bool map_up(CUtensorMap* m, const void* base, const muon_experts_t* a, const WeightPlan& w) {
@@ -425,6 +445,7 @@ ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const Api
   p.experts = a->experts;
   p.pad = pad;
   p.inner = static_cast<int>(a->inner), p.ip = static_cast<int>(w.ip);
+  p.ap = p.ip, p.gp = 2 * p.ip;
   p.status = d.status, p.timeout_ns = d.timeout_ns;
   return p;
 }
@@ -492,8 +513,8 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   ExGemmParams down = gemm_params(a, w, d, 1);
   down.m_tiles = tiles_of(H, kExMTile), down.kb = tiles_of(I, 64), down.m = static_cast<int>(H);
   down.y = y, down.yp = yp;
-  if (!map_up(&up.mapA, w_in, a, w) || !map2(&up.mapB, xp, H, rows, w.hp, 32) ||
-      !map3(&down.mapA, w_out, I, H, a->experts, w.ip, 128) || !map2(&down.mapB, act, I, rows, w.ip, 32))
+  if (!map_up(&up.mapA, w_in, a, w) || !map_rows(&up, xp, H, rows, w.hp) ||
+      !map3(&down.mapA, w_out, I, H, a->experts, w.ip, 128) || !map_rows(&down, act, I, rows, w.ip))
     return MUON_ERR_CUDA;
   MUON_TRY(c.run(launch_ex_gemm(kExUp, up, d.sms, stream)));
   MUON_TRY(c.run(launch_ex_gemm(kExDown, down, d.sms, stream)));
@@ -534,8 +555,11 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   // padded rows: every expert with rows adds at most kExSeg - 1
   const int64_t prows = rows + (kExSeg - 1) * std::min<int64_t>(a->experts, rows);
   const int parts = tiles_of(I, kExMTile) * 8;
-  const size_t at_x = cv.take(prows * w.hp * 2), at_d = cv.take(prows * w.hp * 2), at_wr = cv.take(prows * 4),
-               at_dgu = cv.take(prows * 2 * w.ip * 2), at_wa = cv.take(prows * w.ip * 2),
+  // pitches of whole 64-column chunks (map_mn); the columns past the data
+  // reach only results that are not stored
+  const int64_t xpitch = rup(H, 64), gpitch = rup(2 * w.ip, 64), apitch = rup(w.ip, 64);
+  const size_t at_x = cv.take(prows * xpitch * 2), at_d = cv.take(prows * xpitch * 2), at_wr = cv.take(prows * 4),
+               at_dgu = cv.take(prows * gpitch * 2), at_wa = cv.take(prows * apitch * 2),
                at_part = cv.take(rows * parts * 4), at_y = dx ? cv.take(rows * yp * 4) : 0;
   char* ws = nullptr;
   MUON_TRY(workspace(stream, cv.bytes, &ws));
@@ -552,6 +576,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   g.x[1] = static_cast<const __nv_bfloat16*>(dout), g.xs[1] = dos, g.out[1] = dop;
   g.weights = a->weights;
   g.wr = reinterpret_cast<float*>(ws + at_wr);
+  g.hp = xpitch;
   g.vec = v.x.rows16() && vd.rows16();
   MUON_TRY(c.run(launch_ex_gather(g, prows, stream)));
   ExGemmParams da = gemm_params(a, w, d, kExSeg);
@@ -559,8 +584,9 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   da.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));
   da.gu_vec = aligned(gu, 16) && I % 8 == 0;
   da.wr = g.wr, da.dgu = dgu, da.act = wact;
+  da.ap = static_cast<int>(apitch), da.gp = static_cast<int>(gpitch);
   da.part = reinterpret_cast<float*>(ws + at_part);
-  if (!map3(&da.mapA, w_out, I, H, a->experts, w.ip, 64) || !map2(&da.mapB, dop, H, prows, w.hp, 32))
+  if (!map_weights_mn(&da, w_out, I, H, w.ip) || !map_rows(&da, dop, H, prows, xpitch))
     return MUON_ERR_CUDA;
   MUON_TRY(c.run(launch_ex_gemm(kExDact, da, d.sms, stream)));
   if (dweights) {
@@ -571,8 +597,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
     ExGemmParams p = gemm_params(a, w, d, kExSeg);
     p.m_tiles = tiles_of(H, kExMTile), p.kb = tiles_of(2 * w.ip, 64), p.m = static_cast<int>(H);
     p.y = reinterpret_cast<float*>(ws + at_y), p.yp = yp;
-    if (!map3(&p.mapA, w_in, H, 2 * w.ip, a->experts, w.hp, 64) ||
-        !map2(&p.mapB, dgu, 2 * w.ip, prows, 2 * w.ip, 32))
+    if (!map_weights_mn(&p, w_in, H, 2 * w.ip, w.hp) || !map_rows(&p, dgu, 2 * w.ip, prows, gpitch))
       return MUON_ERR_CUDA;
     MUON_TRY(c.run(launch_ex_gemm(kExDx, p, d.sms, stream)));
     MUON_TRY(c.run(launch_ex_combine(combine_params(a, p.y, yp, nullptr, ox), stream)));
@@ -585,8 +610,8 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
     p.m_tiles = tiles_of(p.m, kExMTile), p.n_tiles = tiles_of(p.n, kExNTile);
     p.dw = out, p.dw_dt = dw_dt;
     p.dw_vec = aligned(out, 16) && p.n * esize(dw_dt) % 16 == 0;
-    if (!map2(&p.mapA, k ? dop : dgu, p.m, prows, k ? w.hp : 2 * w.ip, 64) ||
-        !map2(&p.mapB, k ? wact : xp, p.n, prows, k ? w.ip : w.hp, 64))
+    const int64_t ap = k ? xpitch : gpitch, bp = k ? apitch : xpitch;
+    if (!map_mn(&p.mapA, k ? dop : dgu, ap, prows, ap, 0) || !map_mn(&p.mapB, k ? wact : xp, bp, prows, bp, 0))
       return MUON_ERR_CUDA;
     MUON_TRY(c.run(launch_ex_gemm(k ? kExDwOut : kExDwIn, p, d.sms, stream)));
   }

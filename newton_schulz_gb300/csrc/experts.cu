@@ -16,7 +16,12 @@
 // One CTA pair (a cluster of two) per tile of 256 (M) x N: tcgen05.mma with
 // cta_group::2, each CTA holding 128 rows of A, half of B's columns and 128
 // rows of D, so 32 KB of operands feed each SM per 128 x 256 x 64 block.  Per CTA:
-//   warp 0      TMA producer, a ring of five 32 KB stages (128-byte swizzle);
+//   warp 0      TMA producer, a ring of six 32 KB stages (128-byte swizzle),
+//               one copy per operand and stage: the copy engine's cost per
+//               instruction shows (B in four boxes of 32 rows instead of one of
+//               128: 1428 against 1207 us for 4093 tokens' up product over
+//               8 x [28672, 4096]), which also rules out gathering the rows by
+//               four in the copy, 32 instructions a stage;
 //   warp 1      TMEM; in the pair's CTA 0 it issues the MMAs of both;
 //   warps 2..9  epilogue, two sets of four (128 TMEM lanes each) that take
 //               the accumulator's column slabs in turn.
@@ -47,10 +52,9 @@ namespace {
 constexpr int BK = 64, UMMA_K = 16;
 constexpr int kOpBytes = 128 * BK * 2;          // one CTA's A or B of a stage
 constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kStages = 5;
-constexpr int kSetBytes = 16 * 1024;            // epilogue staging per set
-constexpr int kBarOff = kStages * kStageBytes + 2 * kSetBytes;
-constexpr int kScanOff = kBarOff + 256;
+constexpr int kMostStages = 6;
+constexpr int kBarBytes = 256;
+constexpr int kSmemLimit = 227 * 1024;
 constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;
 constexpr unsigned kFull = 0xffffffffu;
@@ -58,23 +62,33 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr bool is_dw(int kind) { return kind == kExDwIn || kind == kExDwOut; }
 constexpr bool a_mn(int kind) { return kind >= kExDact; }   // A read MN-major
 
-int gemm_smem(int experts) { return kScanOff + 3 * (experts + 1) * 4 + 1024; }
+// epilogue staging per set
+constexpr int set_bytes(int kind) { return is_dw(kind) ? 16 * 1024 : 12 * 1024; }
+int gemm_smem(int kind, int stages, int experts) {
+  return stages * kStageBytes + 2 * set_bytes(kind) + kBarBytes + 3 * (experts + 1) * 4 + 1024;
+}
 
 // First row of every expert in the plan (off), in the padded numbering (poff)
-// and its number of row tiles (tt, running), by one warp.
+// and its number of row tiles (tt, running).
 struct Scan {
   int *off, *poff, *tt;    // [experts + 1]
 };
 
 __device__ __forceinline__ int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
-__device__ __forceinline__ void scan_offsets(const Scan& s, const int32_t* offsets, int experts,
-                                             int64_t rows, int pad, bool tile_pads, int lane) {
+// All threads of the block: offsets into s.off, clamped; then, after a barrier,
+// one warp scans.
+__device__ __forceinline__ void fetch_offsets(const Scan& s, const int32_t* offsets, int experts,
+                                              int64_t rows) {
+  for (int e = threadIdx.x; e <= experts; e += blockDim.x)
+    s.off[e] = max(0, static_cast<int>(min(static_cast<int64_t>(offsets[e]), rows)));
+}
+
+__device__ __forceinline__ void scan_offsets(const Scan& s, int experts, int pad, bool tile_pads, int lane) {
   int top = 0, pbase = 0, tbase = 0;
   for (int e0 = 0; e0 <= experts; e0 += 32) {
     const int e = e0 + lane;
-    int v = e <= experts ? offsets[e] : 0;
-    v = max(0, static_cast<int>(min(static_cast<int64_t>(v), rows)));
+    int v = e <= experts ? s.off[e] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(kFull, v, o);
@@ -292,7 +306,7 @@ __device__ __forceinline__ void epi_up(const ExGemmParams& p, const Tile& t, con
     for (int k = 0; k < 2; ++k) {
       const int row = (w.tid >> 3) + 16 * k, chunk = w.tid & 7, ft = f0 + chunk * 8;
       if (c0 + row >= t.rows) continue;
-      store8(p.act + static_cast<int64_t>(t.prow + c0 + row) * p.ip + ft,
+      store8(p.act + static_cast<int64_t>(t.prow + c0 + row) * p.ap + ft,
              lds16(staged(w.stg, row, chunk, 128)), p.ip - ft, true);
       if (p.gu) {
         __nv_bfloat16* o = p.gu + static_cast<int64_t>(t.urow + c0 + row) * 2 * p.inner + ft;
@@ -403,9 +417,9 @@ __device__ __forceinline__ void epi_dact(const ExGemmParams& p, const Tile& t, c
       const int row = tok + 8 * k;
       if (c0 + row >= t.rows) continue;
       const int64_t at = t.prow + c0 + row;
-      store8(p.dgu + at * 2 * p.ip + ft, lds16(staged(w.stg, row, chunk, 256)), p.ip - ft, true);
-      store8(p.dgu + at * 2 * p.ip + p.ip + ft, lds16(staged(w.stg + 4096, row, chunk, 256)), p.ip - ft, true);
-      store8(p.act + at * p.ip + ft, lds16(staged(w.stg + 8192, row, chunk, 256)), p.ip - ft, true);
+      store8(p.dgu + at * p.gp + ft, lds16(staged(w.stg, row, chunk, 256)), p.ip - ft, true);
+      store8(p.dgu + at * p.gp + p.ip + ft, lds16(staged(w.stg + 4096, row, chunk, 256)), p.ip - ft, true);
+      store8(p.act + at * p.ap + ft, lds16(staged(w.stg + 8192, row, chunk, 256)), p.ip - ft, true);
     }
     w.bar();
   }
@@ -485,9 +499,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ex_gemm_kernel(const __grid_constant__ ExGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int kStages = p.stages;
   uint8_t* sStage = smem;
   uint8_t* sEpi = smem + kStages * kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);   // CTA 0's count for both
+  uint8_t* sBar = sEpi + 2 * set_bytes(KIND);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sBar);   // CTA 0's count for both
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;     // [2] accumulator ready
   uint64_t* tempty = tfull + 2;          // [2] accumulator drained by both CTAs (CTA 0's)
@@ -496,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_ok = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2 sets][2]
   Scan scan;
-  scan.off = reinterpret_cast<int*>(smem + kScanOff);
+  scan.off = reinterpret_cast<int*>(sBar + kBarBytes);
   scan.poff = scan.off + p.experts + 1;
   scan.tt = scan.poff + p.experts + 1;
 
@@ -518,9 +534,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&p.mapA);
     ptx::prefetch_tmap(&p.mapB);
+    if (!is_dw(KIND)) ptx::prefetch_tmap(&p.mapB32);
   }
   if (warp == 1) ptx::tmem_alloc_pair(tmem_slot, kTmemCols);
-  if (warp == 2) scan_offsets(scan, p.offsets, p.experts, p.rows, p.pad, KIND == kExDact, lane);
+  fetch_offsets(scan, p.offsets, p.experts, p.rows);
+  __syncthreads();
+  if (warp == 2) scan_offsets(scan, p.experts, p.pad, KIND == kExDact, lane);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();     // both CTAs' barriers are initialised
@@ -536,8 +555,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool stop = false;
       for (int tile = tile0; tile < tiles && !stop; tile += tstep) {
         const Tile t = decode<KIND>(p, scan, tile);
-        const int half = t.cols / 2, boxes = (half + 31) / 32;
-        const uint32_t bytes = is_dw(KIND) ? 2 * kStageBytes : 2 * (kOpBytes + boxes * 4096);
+        // B: one box of 128 rows, or one or two of 32 for a small tile
+        const int half = t.cols / 2, boxes = half > 64 ? 0 : (half + 31) / 32;
+        const uint32_t bytes = 2 * (kOpBytes + (boxes ? boxes * 4096 : kOpBytes));
         const int m0 = t.m * kExMTile + crank * 128;
         for (int i = 0; i < t.kb; ++i) {
           if (!wait_bounded(&empty[stage], phase ^ 1, abort_flag, p.status, p.timeout_ns, true)) {
@@ -555,22 +575,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           } else if (KIND == kExDown) {
             ptx::tma_load_3d_pair(a, &p.mapA, bar, k, m0, t.e);
           } else if (is_dw(KIND)) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              ptx::tma_load_2d_pair(a + h * 8192, &p.mapA, bar, m0 + 64 * h, t.prow + k);
+            ptx::tma_load_3d_pair(a, &p.mapA, bar, 0, t.prow + k, m0 / 64);
+          } else if (p.a_whole) {
+            ptx::tma_load_4d_pair(a, &p.mapA, bar, 0, k, m0 / 64, t.e);
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               ptx::tma_load_3d_pair(a + h * 8192, &p.mapA, bar, m0 + 64 * h, k, t.e);
           }
           if (is_dw(KIND)) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              ptx::tma_load_2d_pair(b + h * 8192, &p.mapB, bar, t.n * kExNTile + crank * 128 + 64 * h,
-                                    t.prow + k);
+            ptx::tma_load_3d_pair(b, &p.mapB, bar, 0, t.prow + k, t.n * 4 + crank * 2);
+          } else if (boxes == 0) {
+            ptx::tma_load_2d_pair(b, &p.mapB, bar, k, t.prow + crank * half);
           } else {
             for (int h = 0; h < boxes; ++h)
-              ptx::tma_load_2d_pair(b + h * 4096, &p.mapB, bar, k, t.prow + crank * half + 32 * h);
+              ptx::tma_load_2d_pair(b + h * 4096, &p.mapB32, bar, k, t.prow + crank * half + 32 * h);
           }
           ++issued;
           if (++stage == kStages) {
@@ -638,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     w.set = (warp - 2) >> 2;
     w.lane = lane;
     w.tid = ((warp - 2) & 3) * 32 + lane;
-    w.stg = ptx::smem_u32(sEpi + w.set * kSetBytes);
+    w.stg = ptx::smem_u32(sEpi + w.set * set_bytes(KIND));
     int acc = 0;
     for (int tile = tile0, it = 0; tile < tiles; tile += tstep, ++it) {
       const Tile t = decode<KIND>(p, scan, tile);
@@ -673,7 +692,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) ptx::tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-// Copies the rows of x (and dout) into expert order, a warp per row; HBM-bound.
+// Copies the rows of x (and dout) into expert order, a warp per row, four
+// 16-byte loads a lane in flight; HBM-bound (every row of x is read top_k
+// times, from L2 while x fits there).
 __global__ void __launch_bounds__(256) ex_gather_kernel(const __grid_constant__ ExGatherParams p) {
   extern __shared__ int s_scan[];
   Scan s;
@@ -681,24 +702,38 @@ __global__ void __launch_bounds__(256) ex_gather_kernel(const __grid_constant__ 
   s.poff = s.off + p.experts + 1;
   s.tt = s.poff + p.experts + 1;
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) scan_offsets(s, p.offsets, p.experts, p.rows, p.pad, false, lane);
+  fetch_offsets(s, p.offsets, p.experts, p.rows);
+  __syncthreads();
+  if (threadIdx.x < 32) scan_offsets(s, p.experts, p.pad, false, lane);
   __syncthreads();
   const int total = s.poff[p.experts];
   for (int64_t r = blockIdx.x * 8LL + (threadIdx.x >> 5); r < total; r += gridDim.x * 8LL) {
-    const int e = find(s.poff, p.experts, static_cast<int>(r));
-    const int urow = s.off[e] + static_cast<int>(r) - s.poff[e];
-    int32_t sv = urow < s.off[e + 1] ? p.src[urow] : -1;
+    int urow = static_cast<int>(r);
+    bool live = true;
+    if (p.pad > 1) {
+      const int e = find(s.poff, p.experts, static_cast<int>(r));
+      urow = s.off[e] + static_cast<int>(r) - s.poff[e];
+      live = urow < s.off[e + 1];
+    }
+    int32_t sv = live ? p.src[urow] : -1;
     if (sv >= p.rows) sv = -1;
     const int64_t tok = sv < 0 ? 0 : sv / p.top_k;
     if (p.wr && lane == 0) p.wr[r] = sv < 0 ? 0.f : p.weights[sv];
-#pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (!p.x[q]) continue;
       const __nv_bfloat16* in = p.x[q] + tok * p.xs[q];
       __nv_bfloat16* out = p.out[q] + r * p.hp;
-      for (int64_t c = lane * 8; c < p.hp; c += 256) {
-        const int n = sv < 0 ? 0 : static_cast<int>(min(p.hidden - c, static_cast<int64_t>(8)));
-        *reinterpret_cast<uint4*>(out + c) = load8(in + c, n, p.vec != 0);
+      for (int64_t c0 = lane * 8; c0 < p.hp; c0 += 1024) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t c = c0 + 256 * j;
+          v[j] = load8(in + c, sv < 0 ? 0 : static_cast<int>(min(p.hidden - c, static_cast<int64_t>(8))),
+                       p.vec != 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c0 + 256 * j < p.hp) *reinterpret_cast<uint4*>(out + c0 + 256 * j) = v[j];
       }
     }
   }
@@ -768,8 +803,10 @@ __global__ void __launch_bounds__(256)
 namespace {
 
 template <int KIND>
-cudaError_t gemm_launch(const ExGemmParams& p, int sms, cudaStream_t s) {
-  const int smem = gemm_smem(p.experts);
+cudaError_t gemm_launch(ExGemmParams p, int sms, cudaStream_t s) {
+  p.stages = kMostStages;
+  if (gemm_smem(KIND, p.stages, p.experts) > kSmemLimit) p.stages = kMostStages - 1;
+  const int smem = gemm_smem(KIND, p.stages, p.experts);
   const cudaError_t e = cudaFuncSetAttribute(ex_gemm_kernel<KIND>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -793,7 +830,7 @@ cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, cudaStream_
 }
 
 cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, cudaStream_t s) {
-  ex_gather_kernel<<<some((padded_rows + 7) / 8, 2432), 256, 3 * (p.experts + 1) * sizeof(int), s>>>(p);
+  ex_gather_kernel<<<some((padded_rows + 7) / 8, 1216), 256, 3 * (p.experts + 1) * sizeof(int), s>>>(p);
   return cudaGetLastError();
 }
 

@@ -109,72 +109,110 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     }
     if (p.top_groups < p.groups) {
       const int per = p.experts / p.groups;
-      int grp[EPL];
+      const bool sum2 = p.group_score == 1;
+      // what a group is ranked by, as ordered words
+      uint32_t rank[EPL];
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) grp[i] = (i * 32 + lane) / per;
+      for (int i = 0; i < EPL; ++i) rank[i] = sum2 && !p.bias && key[i] ? ordered(sc[i]) : key[i];
       uint32_t best[2] = {0u, 0u};     // this lane: groups lane and 32 + lane
-      for (int g = 0; g < p.groups; ++g) {
-        uint32_t a = 0u, b = 0u;       // the two largest of this lane's in the group
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          uint32_t v = grp[i] == g ? key[i] : 0u;
-          if (v && p.group_score == 1 && !p.bias) v = ordered(sc[i]);
-          b = max(b, min(a, v));
-          a = max(a, v);
-        }
+      // a: this lane's largest in the group, b: its second largest
+      auto score_of = [&](uint32_t a, uint32_t b) {
         const uint32_t m1 = __reduce_max_sync(kFull, a);
-        uint32_t score = m1;
-        if (p.group_score == 1 && m1) {
-          const int owner = __ffs(__ballot_sync(kFull, a == m1)) - 1;
-          const uint32_t m2 = __reduce_max_sync(kFull, lane == owner ? b : a);
-          score = ordered(m2 ? unordered(m1) + unordered(m2) : unordered(m1));
-        }
-        if (lane == (g & 31)) {
-          if (g < 32) best[0] = score;
-          else best[1] = score;
+        if (!sum2 || !m1) return m1;
+        const int owner = __ffs(__ballot_sync(kFull, a == m1)) - 1;
+        const uint32_t m2 = __reduce_max_sync(kFull, lane == owner ? b : a);
+        return ordered(m2 ? unordered(m1) + unordered(m2) : unordered(m1));
+      };
+      uint64_t keep = 0;
+      if (per == 32) {
+        // register i is group i
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (i < p.groups) {
+            const uint32_t score = score_of(rank[i], 0u);
+            if (lane == i) best[0] = score;
+          }
+      } else {
+        for (int g = 0; g < p.groups; ++g) {
+          uint32_t a = 0u, b = 0u;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) {
+            const int e = i * 32 + lane - g * per;
+            const uint32_t v = e >= 0 && e < per ? rank[i] : 0u;
+            b = max(b, min(a, v));
+            a = max(a, v);
+          }
+          const uint32_t score = score_of(a, b);
+          if (lane == (g & 31)) {
+            if (g < 32) best[0] = score;
+            else best[1] = score;
+          }
         }
       }
-      uint64_t keep = 0;
       for (int j = 0; j < p.top_groups; ++j) {
         const uint32_t m = __reduce_max_sync(kFull, max(best[0], best[1]));
         if (!m) break;
-        const uint32_t cand = best[0] == m ? lane : best[1] == m ? 32u + lane : 64u;
-        const uint32_t g = __reduce_min_sync(kFull, cand);
+        const unsigned lo = __ballot_sync(kFull, best[0] == m), hi = __ballot_sync(kFull, best[1] == m);
+        const int g = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
         keep |= 1ull << g;
         if (lane == (g & 31)) {
           if (g < 32) best[0] = 0u;
           else best[1] = 0u;
         }
       }
+      if (per == 32) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i * 32 + lane < p.experts && !((keep >> grp[i]) & 1)) key[i] = 0u;
+        for (int i = 0; i < EPL; ++i)
+          if (!((keep >> i) & 1)) key[i] = 0u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const int e = i * 32 + lane;
+          if (e < p.experts && !((keep >> (e / per)) & 1)) key[i] = 0u;
+        }
+      }
     }
-    for (int j = 0; j < k; ++j) {
-      uint32_t a = key[0];
-      int at = 0;
+    // this lane's largest key, the lowest expert among equal ones
+    uint32_t a;
+    int at;
+    auto rescan = [&] {
+      a = key[0];
+      at = 0;
 #pragma unroll
       for (int i = 1; i < EPL; ++i)
         if (key[i] > a) {
           a = key[i];
           at = i;
         }
+    };
+    rescan();
+    for (int j = 0; j < k; ++j) {
       const uint32_t m = __reduce_max_sync(kFull, a);
       if (!m) break;
-      const uint32_t e = __reduce_min_sync(kFull, a == m ? static_cast<uint32_t>(at * 32 + lane) : ~0u);
-      const int owner = e & 31;
+      const unsigned who = __ballot_sync(kFull, a == m);
+      int owner = __ffs(who) - 1;
+      int e = __shfl_sync(kFull, at, owner) * 32 + owner;
+      if (who & (who - 1)) {      // equal keys in several lanes
+        e = static_cast<int>(__reduce_min_sync(kFull, a == m ? static_cast<uint32_t>(at * 32 + lane) : ~0u));
+        owner = e & 31;
+      }
+      if (lane == j) my_idx = e;
+      if (lane == owner) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (i == at) key[i] = 0u;
+        rescan();
+      }
+    }
+    // the chosen experts' scores, from their lanes
+    for (int j = 0; j < k; ++j) {
+      const int e = __shfl_sync(kFull, my_idx, j);
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (i == at) {
-          s = sc[i];
-          if (lane == owner) key[i] = 0u;
-        }
-      s = __shfl_sync(kFull, s, owner);
-      if (lane == j) {
-        my_idx = static_cast<int32_t>(e);
-        my_score = s;
-      }
+        if (i == (e >> 5)) s = sc[i];
+      s = __shfl_sync(kFull, s, e & 31);
+      if (lane == j && e >= 0) my_score = s;
     }
   }
   if (p.renorm) {
@@ -197,8 +235,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   load_logits<EPL>(x, p.logits, p.dtype, tok * p.stride, p.experts, lane);
   if (p.score == 0) {
     const float sum = softmax_parts<EPL>(x, sc);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) sc[i] = sum > 0.f ? sc[i] / sum : 0.f;
+    for (int i = 0; i < EPL; ++i) sc[i] *= inv;
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sc[i] = sigmoid(x[i]);
