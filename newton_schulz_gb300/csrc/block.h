@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "muon_internal.h"
 
@@ -25,6 +26,25 @@ std::mutex& api_mutex();
 int api_device(ApiDevice* out);                                          // muon_status_t
 int api_workspace(cudaStream_t stream, size_t bytes, char** out);        // muon_status_t
 void api_set_launches(int n);
+
+// Launch of a kernel that follows another of the same call: it may start while
+// that one ends (programmatic dependent launch), and waits for its results
+// with ptx::wait_dependency before it touches what the call's kernels share.
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                         typename std::common_type<A>::type... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // ---- RMS norm --------------------------------------------------------------------------
 constexpr int kNormMaxCols = 32768;
@@ -109,8 +129,9 @@ struct PlanParams {
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t s);
 cudaError_t launch_route_grad(const RouteGradParams& p, cudaStream_t s);
-cudaError_t launch_plan_hist(const PlanParams& p, cudaStream_t s);
-cudaError_t launch_plan(const PlanParams& p, cudaStream_t s);
+// after: the launch follows another of the same call (launch_after)
+cudaError_t launch_plan_hist(const PlanParams& p, bool after, cudaStream_t s);
+cudaError_t launch_plan(const PlanParams& p, bool after, cudaStream_t s);
 
 // ---- experts' products ---------------------------------------------------------------------
 // Products on the tensor cores (experts.cu), by operand and result.
@@ -141,8 +162,10 @@ struct ExGemmParams {
   __nv_bfloat16* act;             // [padded rows][ap]: kExUp act, kExDact w a
   __nv_bfloat16* gu;              // [rows][2 inner]: kExUp output or null, kExDact input
   int gu_vec;                     // 16-byte accesses to gu are legal
-  float* y;                       // [rows][yp]
+  int16_t* y;                     // [rows][yp] scaled integers
   int64_t yp;
+  uint8_t* yexp;                  // [rows][yep] exponents, one per 32 columns
+  int64_t yep;
   const float* wr;                // [padded rows] weight of a row
   __nv_bfloat16* dgu;             // [padded rows][gp], gate part then up part at ip
   float* part;                    // [m_tiles * 8][rows] parts of dweights
@@ -169,8 +192,10 @@ struct ExGatherParams {
 };
 
 struct ExCombineParams {          // out[t] = sum_j w[t,j] y[pos[t,j]]
-  const float* y;
+  const int16_t* y;               // as ExGemmParams wrote it
   int64_t yp;
+  const uint8_t* yexp;
+  int64_t yep;
   const int32_t* pos;
   const float* weights;           // null: ones
   __nv_bfloat16* out;
@@ -186,9 +211,29 @@ struct ExWeightParams {           // dweights[t,j] = sum over parts of part[.][p
   int parts;
 };
 
+// A few rows: matrix-vector products, two launches, no padding or copies.
+constexpr int kExFewRows = 32;
+struct ExFewParams {
+  const __nv_bfloat16* x;
+  int64_t xs;
+  const __nv_bfloat16* w_in;      // [experts][2 inner][hidden]
+  const __nv_bfloat16* w_out;     // [experts][hidden][inner]
+  const float* weights;
+  const int32_t* offsets;
+  const int32_t* src;
+  const int32_t* pos;
+  __nv_bfloat16* gu;              // [rows][2 inner] or null
+  __nv_bfloat16* act;             // [rows][ip], 16-byte aligned rows
+  __nv_bfloat16* out;
+  int64_t outs, tokens, ip;
+  int hidden, inner, experts, top_k, rows;
+  int vec_in, vec_out;            // 16-byte loads of x and w_in, of w_out
+};
+cudaError_t launch_ex_few(const ExFewParams& p, cudaStream_t s);    // two launches
+
 cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, cudaStream_t s);
 cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, cudaStream_t s);
-cudaError_t launch_ex_combine(const ExCombineParams& p, cudaStream_t s);
+cudaError_t launch_ex_combine(const ExCombineParams& p, int sms, cudaStream_t s);
 cudaError_t launch_ex_dweights(const ExWeightParams& p, cudaStream_t s);
 // mats matrices [rows][cols] -> [rows_p][cols_p], zeros around
 cudaError_t launch_ex_repack(const __nv_bfloat16* in, int64_t mats, int64_t rows, int64_t cols,

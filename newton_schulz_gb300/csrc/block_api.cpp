@@ -182,8 +182,8 @@ bool unsupported_route(int64_t tokens, int top_k, int experts, int groups) {
 
 // The plan's launches; hist: workspace, unused with one tile.
 muon_status_t plan_launches(const PlanParams& p, Counter* c, cudaStream_t stream) {
-  if (p.tiles > 1) MUON_TRY(c->run(launch_plan_hist(p, stream)));
-  return c->run(launch_plan(p, stream));
+  if (p.tiles > 1) MUON_TRY(c->run(launch_plan_hist(p, c->n > 0, stream)));
+  return c->run(launch_plan(p, c->n > 0, stream));
 }
 
 PlanParams plan_params(const int32_t* idx, int64_t tokens, int top_k, int experts, int32_t* offsets,
@@ -460,17 +460,31 @@ ExGatherParams gather_params(const muon_experts_t* a, const WeightPlan& w, int p
   return g;
 }
 
-ExCombineParams combine_params(const muon_experts_t* a, const float* y, int64_t yp, const float* weights,
+ExCombineParams combine_params(const muon_experts_t* a, const ExGemmParams& g, const float* weights,
                                const View& out) {
   ExCombineParams p;
   std::memset(&p, 0, sizeof(p));
-  p.y = y, p.yp = yp, p.pos = a->pos, p.weights = weights;
+  p.y = g.y, p.yp = g.yp, p.yexp = g.yexp, p.yep = g.yep, p.pos = a->pos, p.weights = weights;
   p.out = static_cast<__nv_bfloat16*>(const_cast<void*>(out.p));
   p.outs = out.stride, p.tokens = a->tokens, p.hidden = a->hidden, p.rows = a->tokens * a->top_k;
   p.top_k = a->top_k;
-  p.vec = aligned(out.p, 8) && (out.rows <= 1 || out.stride % 4 == 0);
+  p.vec = out.rows16();
   return p;
 }
+
+// The rows that are summed over slots: 16-bit values, an exponent per 32.
+struct RowPlan {
+  int64_t yp, yep;
+  size_t at_y, at_e;
+  RowPlan(int64_t rows, int64_t hidden, Carve* c) : yp(rup(hidden, 8)), yep(rup(hidden, 256) / 32) {
+    at_y = c->take(rows * yp * 2);
+    at_e = c->take(rows * yep);
+  }
+  void set(ExGemmParams* p, char* ws) const {
+    p->y = reinterpret_cast<int16_t*>(ws + at_y), p->yp = yp;
+    p->yexp = reinterpret_cast<uint8_t*>(ws + at_e), p->yep = yep;
+  }
+};
 
 int tiles_of(int64_t n, int64_t per) { return static_cast<int>((n + per - 1) / per); }
 
@@ -490,15 +504,36 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   ApiDevice d;
   MUON_TRY(device(&d));
   Carve cv;
+  Counter c;
+  if (rows <= kExFewRows) {
+    // The tile kernels' latency (launches, a ring to fill, tiles for a part of
+    // the SMs) against the weights' bytes per row.
+    const int64_t ip = rup(I, 8);
+    const size_t at = cv.take(rows * ip * 2);
+    char* ws = nullptr;
+    MUON_TRY(workspace(stream, cv.bytes, &ws));
+    ExFewParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = static_cast<const __nv_bfloat16*>(a->x), p.xs = a->x_stride;
+    p.w_in = static_cast<const __nv_bfloat16*>(a->w_in), p.w_out = static_cast<const __nv_bfloat16*>(a->w_out);
+    p.weights = a->weights, p.offsets = a->offsets, p.src = a->src, p.pos = a->pos;
+    p.gu = static_cast<__nv_bfloat16*>(gu), p.act = reinterpret_cast<__nv_bfloat16*>(ws + at);
+    p.out = static_cast<__nv_bfloat16*>(out), p.outs = outs;
+    p.tokens = a->tokens, p.ip = ip, p.rows = static_cast<int>(rows);
+    p.hidden = static_cast<int>(H), p.inner = static_cast<int>(I), p.experts = a->experts, p.top_k = a->top_k;
+    p.vec_in = v.x.rows16() && aligned(a->w_in, 16) && H % 8 == 0;
+    p.vec_out = aligned(a->w_out, 16) && I % 8 == 0;
+    MUON_TRY(c.run(launch_ex_few(p, stream)));
+    api_set_launches(2);
+    return MUON_OK;
+  }
   const WeightPlan w(a, &cv);
-  const int64_t yp = rup(H, 4);
-  const size_t at_x = cv.take(rows * w.hp * 2), at_act = cv.take(rows * w.ip * 2), at_y = cv.take(rows * yp * 4);
+  const RowPlan rp(rows, H, &cv);
+  const size_t at_x = cv.take(rows * w.hp * 2), at_act = cv.take(rows * w.ip * 2);
   char* ws = nullptr;
   MUON_TRY(workspace(stream, cv.bytes, &ws));
   __nv_bfloat16* xp = reinterpret_cast<__nv_bfloat16*>(ws + at_x);
   __nv_bfloat16* act = reinterpret_cast<__nv_bfloat16*>(ws + at_act);
-  float* y = reinterpret_cast<float*>(ws + at_y);
-  Counter c;
   const __nv_bfloat16 *w_in, *w_out;
   MUON_TRY(pack_weights(a, w, ws, &w_in, &w_out, &c, stream));
   ExGatherParams g = gather_params(a, w, 1);
@@ -512,13 +547,13 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   up.gu_vec = aligned(gu, 16) && I % 8 == 0;
   ExGemmParams down = gemm_params(a, w, d, 1);
   down.m_tiles = tiles_of(H, kExMTile), down.kb = tiles_of(I, 64), down.m = static_cast<int>(H);
-  down.y = y, down.yp = yp;
+  rp.set(&down, ws);
   if (!map_up(&up.mapA, w_in, a, w) || !map_rows(&up, xp, H, rows, w.hp) ||
       !map3(&down.mapA, w_out, I, H, a->experts, w.ip, 128) || !map_rows(&down, act, I, rows, w.ip))
     return MUON_ERR_CUDA;
   MUON_TRY(c.run(launch_ex_gemm(kExUp, up, d.sms, stream)));
   MUON_TRY(c.run(launch_ex_gemm(kExDown, down, d.sms, stream)));
-  MUON_TRY(c.run(launch_ex_combine(combine_params(a, y, yp, a->weights, o), stream)));
+  MUON_TRY(c.run(launch_ex_combine(combine_params(a, down, a->weights, o), d.sms, stream)));
   api_set_launches(c.n);
   return MUON_OK;
 }
@@ -551,7 +586,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   MUON_TRY(device(&d));
   Carve cv;
   const WeightPlan w(a, &cv);
-  const int64_t yp = rup(H, 4);
+  const RowPlan rp(dx ? rows : 0, H, &cv);
   // padded rows: every expert with rows adds at most kExSeg - 1
   const int64_t prows = rows + (kExSeg - 1) * std::min<int64_t>(a->experts, rows);
   const int parts = tiles_of(I, kExMTile) * 8;
@@ -560,7 +595,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   const int64_t xpitch = rup(H, 64), gpitch = rup(2 * w.ip, 64), apitch = rup(w.ip, 64);
   const size_t at_x = cv.take(prows * xpitch * 2), at_d = cv.take(prows * xpitch * 2), at_wr = cv.take(prows * 4),
                at_dgu = cv.take(prows * gpitch * 2), at_wa = cv.take(prows * apitch * 2),
-               at_part = cv.take(rows * parts * 4), at_y = dx ? cv.take(rows * yp * 4) : 0;
+               at_part = cv.take(rows * parts * 4);
   char* ws = nullptr;
   MUON_TRY(workspace(stream, cv.bytes, &ws));
   __nv_bfloat16* xp = reinterpret_cast<__nv_bfloat16*>(ws + at_x);
@@ -596,11 +631,11 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   if (dx) {
     ExGemmParams p = gemm_params(a, w, d, kExSeg);
     p.m_tiles = tiles_of(H, kExMTile), p.kb = tiles_of(2 * w.ip, 64), p.m = static_cast<int>(H);
-    p.y = reinterpret_cast<float*>(ws + at_y), p.yp = yp;
+    rp.set(&p, ws);
     if (!map_weights_mn(&p, w_in, H, 2 * w.ip, w.hp) || !map_rows(&p, dgu, 2 * w.ip, prows, gpitch))
       return MUON_ERR_CUDA;
     MUON_TRY(c.run(launch_ex_gemm(kExDx, p, d.sms, stream)));
-    MUON_TRY(c.run(launch_ex_combine(combine_params(a, p.y, yp, nullptr, ox), stream)));
+    MUON_TRY(c.run(launch_ex_combine(combine_params(a, p, nullptr, ox), d.sms, stream)));
   }
   for (int k = 0; k < 2; ++k) {
     void* out = k ? dw_out : dw_in;

@@ -21,7 +21,10 @@
 //               instruction shows (B in four boxes of 32 rows instead of one of
 //               128: 1428 against 1207 us for 4093 tokens' up product over
 //               8 x [28672, 4096]), which also rules out gathering the rows by
-//               four in the copy, 32 instructions a stage;
+//               four in the copy, 32 instructions a stage.  Warps that gathered
+//               16 bytes a thread straight into the stage took 0.5 us a stage
+//               against 0.39 from a copy of the rows in expert order, more than
+//               that copy costs;
 //   warp 1      TMEM; in the pair's CTA 0 it issues the MMAs of both;
 //   warps 2..9  epilogue, two sets of four (128 TMEM lanes each) that take
 //               the accumulator's column slabs in turn.
@@ -58,6 +61,8 @@ constexpr int kSmemLimit = 227 * 1024;
 constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;
 constexpr unsigned kFull = 0xffffffffu;
+// least exponent of a piece of rows: its factors both ways are normal numbers
+constexpr uint32_t kExpLeast = 14;
 
 constexpr bool is_dw(int kind) { return kind == kExDwIn || kind == kExDwOut; }
 constexpr bool a_mn(int kind) { return kind >= kExDact; }   // A read MN-major
@@ -318,19 +323,69 @@ __device__ __forceinline__ void epi_up(const ExGemmParams& p, const Tile& t, con
   }
 }
 
-// fp32 rows: lane = feature, so a warp's store is one full 128-byte line
+// Rows for the sum over slots, as 16-bit integers (plus 2^15) with one exponent
+// per row and 32 features (a warp's lanes): q = v * 2^(13 - e), e the exponent of
+// the piece's largest value.  The error, 2^-15 of that largest value, is far below
+// the bf16 rounding of the sum, where bf16 rows would add as much again, and
+// half of fp32's bytes are written and read (16384 tokens over
+// 256 x [768, 2048]: 398 + 167 us with fp32 rows).  A piece that holds an
+// infinity or NaN is NaN.
 __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
-  const int h = w.m0 + w.q4 * 32 + w.lane;
+  const int piece = (w.m0 >> 5) + w.q4;
   for (int c0 = w.set * 32; c0 < t.rows; c0 += 64) {
-    uint32_t r[32];
-    ptx::tmem_ld_32x32b_x32(w.taddr + c0, r);
+    uint32_t r[2][16];
+    ptx::tmem_ld_16x256b_x4(w.taddr + c0, r[0]);
+    ptx::tmem_ld_16x256b_x4(w.taddr + (16u << 16) + c0, r[1]);
     ptx::tmem_ld_wait();
-    if (h < p.m) {
-      float* o = p.y + static_cast<int64_t>(t.urow + c0) * p.yp + h;
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (c0 + j < t.rows) o[j * p.yp] = f(r[j]);
+    for (int i = 0; i < 4; ++i) {
+      // rows 8 i + 2 (lane % 4) (low half) and the next (high half): upper
+      // 16 bits of the magnitudes, largest over this thread's 4 features, then the warp's 32
+      uint32_t m = 0;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          m = __vmaxu2(m, __byte_perm(r[b][4 * i + 2 * h], r[b][4 * i + 2 * h + 1], 0x7632) & 0x7fff7fffu);
+      m = __vmaxu2(m, __shfl_xor_sync(kFull, m, 4));
+      m = __vmaxu2(m, __shfl_xor_sync(kFull, m, 8));
+      m = __vmaxu2(m, __shfl_xor_sync(kFull, m, 16));
+      const uint32_t e[2] = {(m >> 7) & 0xffu, m >> 23};
+      float s[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        s[j] = f((267u - min(max(e[j], kExpLeast), 254u)) << 23);
+        const int row = c0 + 8 * i + 2 * (w.lane & 3) + j;
+        if (w.lane < 4 && row < t.rows)
+          p.yexp[(t.urow + row) * p.yep + piece] = static_cast<uint8_t>(max(e[j], kExpLeast));
+      }
+      // adding 2^23 + 2^15 leaves the rounded integer plus 2^15 in the low bits
+      const float big = 8421376.f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t* v = &r[b][4 * i + 2 * h];
+          v[0] = __byte_perm(__float_as_uint(fmaf(f(v[0]), s[0], big)),
+                             __float_as_uint(fmaf(f(v[1]), s[1], big)), 0x5410);
+        }
     }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t q[4] = {r[b][2 * h], r[b][4 + 2 * h], r[b][8 + 2 * h], r[b][12 + 2 * h]};
+        ptx::stmatrix_x4_trans(staged(w.stg, w.lane, w.q4 * 4 + b * 2 + h, 256), q);
+      }
+    w.bar();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = (w.tid >> 4) + 8 * k, chunk = w.tid & 15, h = w.m0 + chunk * 8;
+      if (c0 + row < t.rows && h < p.yp)
+        *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(t.urow + c0 + row) * p.yp + h) =
+            lds16(staged(w.stg, row, chunk, 256));
+    }
+    w.bar();
   }
 }
 
@@ -544,6 +599,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::cluster_sync();     // both CTAs' barriers are initialised
   ptx::tc_fence_after();
+  ptx::launch_dependents();
+  ptx::wait_dependency();
   const uint32_t tmem = *tmem_slot;
   const int tiles = is_dw(KIND) ? p.experts * p.m_tiles * p.n_tiles : scan.tt[p.experts] * p.m_tiles;
 
@@ -693,8 +750,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Copies the rows of x (and dout) into expert order, a warp per row, four
-// 16-byte loads a lane in flight; HBM-bound (every row of x is read top_k
-// times, from L2 while x fits there).
+// 16-byte loads a lane in flight and the next row's token with them; HBM-bound
+// (every row of x is read top_k times, from L2 while x fits there).
 __global__ void __launch_bounds__(256) ex_gather_kernel(const __grid_constant__ ExGatherParams p) {
   extern __shared__ int s_scan[];
   Scan s;
@@ -702,23 +759,30 @@ __global__ void __launch_bounds__(256) ex_gather_kernel(const __grid_constant__ 
   s.poff = s.off + p.experts + 1;
   s.tt = s.poff + p.experts + 1;
   const int lane = threadIdx.x & 31;
+  ptx::launch_dependents();
   fetch_offsets(s, p.offsets, p.experts, p.rows);
   __syncthreads();
   if (threadIdx.x < 32) scan_offsets(s, p.experts, p.pad, false, lane);
   __syncthreads();
   const int total = s.poff[p.experts];
-  for (int64_t r = blockIdx.x * 8LL + (threadIdx.x >> 5); r < total; r += gridDim.x * 8LL) {
-    int urow = static_cast<int>(r);
-    bool live = true;
+  const int step = gridDim.x * 8;
+  // token * top_k + slot of a padded row, -1 where there is none
+  auto source = [&](int r) {
+    if (r >= total) return -1;
+    int urow = r;
     if (p.pad > 1) {
-      const int e = find(s.poff, p.experts, static_cast<int>(r));
-      urow = s.off[e] + static_cast<int>(r) - s.poff[e];
-      live = urow < s.off[e + 1];
+      const int e = find(s.poff, p.experts, r);
+      urow = s.off[e] + r - s.poff[e];
+      if (urow >= s.off[e + 1]) return -1;
     }
-    int32_t sv = live ? p.src[urow] : -1;
-    if (sv >= p.rows) sv = -1;
+    const int32_t v = p.src[urow];
+    return v < p.rows ? v : -1;
+  };
+  int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  int sv = source(r);
+  for (; r < total; r += step) {
+    const int next = source(r + step);
     const int64_t tok = sv < 0 ? 0 : sv / p.top_k;
-    if (p.wr && lane == 0) p.wr[r] = sv < 0 ? 0.f : p.weights[sv];
     for (int q = 0; q < 2; ++q) {
       if (!p.x[q]) continue;
       const __nv_bfloat16* in = p.x[q] + tok * p.xs[q];
@@ -736,47 +800,75 @@ __global__ void __launch_bounds__(256) ex_gather_kernel(const __grid_constant__ 
           if (c0 + 256 * j < p.hp) *reinterpret_cast<uint4*>(out + c0 + 256 * j) = v[j];
       }
     }
+    if (p.wr && lane == 0) p.wr[r] = sv < 0 ? 0.f : p.weights[sv];
+    sv = next;
   }
 }
 
-// out[t] = sum over slots, in slot order, four columns a thread; HBM-bound.
-__global__ void __launch_bounds__(256) ex_combine_kernel(const __grid_constant__ ExCombineParams p) {
-  const int64_t quads = (p.hidden + 3) / 4;
-  const int64_t n = p.tokens * quads;
-  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
-    const int64_t t = i / quads, c = (i - t * quads) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < p.top_k; j0 += 8) {
-      float4 y[8];
-      float w[8];
+// out[t] = sum over slots, in slot order, a block per token, eight columns a
+// lane, SLOTS slots' loads in flight and the next token's rows with them;
+// HBM-bound once the conversions are few (two fp32 operations an instruction, no
+// branch per slot: a slot without a row reads row 0 with weight 0).
+template <int SLOTS>
+__global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constant__ ExCombineParams p) {
+  const int lane = threadIdx.x & 31;
+  const int tokens = static_cast<int>(p.tokens), hidden = static_cast<int>(p.hidden);
+  // this lane's slot of a token: its row, -1 for none, and weight
+  auto slot = [&](int64_t t, int32_t* row, float* w) {
+    *row = -1;
+    *w = 1.f;
+    if (t >= tokens || lane >= p.top_k) return;
+    *row = p.pos[t * p.top_k + lane];
+    if (p.weights) *w = p.weights[t * p.top_k + lane];
+  };
+  ptx::launch_dependents();
+  int32_t next_row;
+  float next_w;
+  slot(blockIdx.x, &next_row, &next_w);
+  ptx::wait_dependency();
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+    const int32_t my_row = next_row < p.rows ? next_row : -1;
+    const float my_w = next_w;
+    slot(t + gridDim.x, &next_row, &next_w);
+    for (int c = threadIdx.x * 8; c - lane * 8 < hidden; c += blockDim.x * 8) {
+      const int cr = min(c, static_cast<int>(p.yp) - 8);      // read column
+      const unsigned live = __ballot_sync(kFull, my_row >= 0);
+      float2 v[4] = {};
+      for (int j0 = 0; j0 < p.top_k; j0 += SLOTS) {
+        uint4 y[SLOTS];
+        uint32_t e[SLOTS];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int32_t r = j0 + j < p.top_k ? p.pos[t * p.top_k + j0 + j] : -1;
-        const bool ok = r >= 0 && r < p.rows;
-        w[j] = !ok ? 0.f : p.weights ? p.weights[t * p.top_k + j0 + j] : 1.f;
-        y[j] = ok ? *reinterpret_cast<const float4*>(p.y + r * p.yp + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < SLOTS; ++j) {
+          const int64_t r = max(__shfl_sync(kFull, my_row, (j0 + j) & 31), 0);
+          y[j] = *reinterpret_cast<const uint4*>(p.y + r * p.yp + cr);
+          e[j] = p.yexp[r * p.yep + (cr >> 5)];
+        }
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+          const float wj = __shfl_sync(kFull, my_w, (j0 + j) & 31);
+          const bool on = j0 + j < 32 && ((live >> (j0 + j)) & 1u);
+          const float w = !on ? 0.f : wj * f(e[j] == 255u ? 0x7fffffffu : (e[j] - 13u) << 23);
+          const float2 w2 = make_float2(w, w), bias = make_float2(-8421376.f, -8421376.f);
+          const uint32_t u[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            // 2^23 + (value + 2^15) from its bits, less that, exactly
+            const float2 x = ptx::add2(make_float2(f(__byte_perm(u[q], 0x4b00u, 0x5410)),
+                                                   f(__byte_perm(u[q], 0x4b00u, 0x5432))), bias);
+            v[q] = ptx::fma2(w2, x, v[q]);
+          }
+        }
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v.x = fmaf(w[j], y[j].x, v.x);
-        v.y = fmaf(w[j], y[j].y, v.y);
-        v.z = fmaf(w[j], y[j].z, v.z);
-        v.w = fmaf(w[j], y[j].w, v.w);
-      }
-    }
-    __nv_bfloat16* o = p.out + t * p.outs + c;
-    if (p.vec && c + 4 <= p.hidden) {
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack(v.x, v.y), pack(v.z, v.w));
-    } else {
-      const float u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (c + j < p.hidden) o[j] = __float2bfloat16_rn(u[j]);
+      const uint4 o = make_uint4(pack(v[0].x, v[0].y), pack(v[1].x, v[1].y), pack(v[2].x, v[2].y),
+                                 pack(v[3].x, v[3].y));
+      store8(p.out + t * p.outs + c, o, hidden - c, p.vec != 0);
     }
   }
 }
 
 __global__ void __launch_bounds__(256) ex_dweights_kernel(const __grid_constant__ ExWeightParams p) {
+  ptx::launch_dependents();
+  ptx::wait_dependency();
   for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < p.rows; i += gridDim.x * 256LL) {
     const int32_t r = p.pos[i];
     float v = 0.f;
@@ -810,8 +902,7 @@ cudaError_t gemm_launch(ExGemmParams p, int sms, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(ex_gemm_kernel<KIND>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  ex_gemm_kernel<KIND><<<sms / 2 * 2, kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(ex_gemm_kernel<KIND>, sms / 2 * 2, kThreads, smem, s, p);
 }
 
 unsigned some(int64_t n, int64_t most) { return static_cast<unsigned>(std::min(std::max<int64_t>(n, 1), most)); }
@@ -834,14 +925,17 @@ cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, cudaS
   return cudaGetLastError();
 }
 
-cudaError_t launch_ex_combine(const ExCombineParams& p, cudaStream_t s) {
-  ex_combine_kernel<<<some((p.tokens * ((p.hidden + 3) / 4) + 255) / 256, 1 << 20), 256, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_ex_combine(const ExCombineParams& p, int sms, cudaStream_t s) {
+  const unsigned warps = some((p.hidden + 255) / 256, 8), block = warps * 32;
+  const unsigned grid = some(p.tokens, static_cast<int64_t>(sms) * (24 / warps));
+  if (p.top_k == 1) return launch_after(ex_combine_kernel<1>, grid, block, 0, s, p);
+  if (p.top_k == 2) return launch_after(ex_combine_kernel<2>, grid, block, 0, s, p);
+  if (p.top_k <= 4) return launch_after(ex_combine_kernel<4>, grid, block, 0, s, p);
+  return launch_after(ex_combine_kernel<8>, grid, block, 0, s, p);
 }
 
 cudaError_t launch_ex_dweights(const ExWeightParams& p, cudaStream_t s) {
-  ex_dweights_kernel<<<some((p.rows + 255) / 256, 1 << 16), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(ex_dweights_kernel, some((p.rows + 255) / 256, 1 << 16), 256, 0, s, p);
 }
 
 cudaError_t launch_ex_repack(const __nv_bfloat16* in, int64_t mats, int64_t rows, int64_t cols,

@@ -80,6 +80,14 @@ __device__ __forceinline__ void to_float(const Chunk<WIDE>& c, int dt, float (&v
   }
 }
 
+template <bool WIDE>
+__device__ __forceinline__ void to_float2(const Chunk<WIDE>& c, int dt, float2 (&v)[4]) {
+  float x[8];
+  to_float<WIDE>(c, dt, x);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = make_float2(x[2 * j], x[2 * j + 1]);
+}
+
 // gain[col .. col + 8), ones where there is none
 __device__ __forceinline__ void load_gain(float (&g)[8], const void* gain, int dt, int col, int cols,
                                           bool vec) {
@@ -418,12 +426,16 @@ __global__ void __launch_bounds__(256, 2)
   __syncthreads();
   if (t == 0)
     for (int64_t k = 0; k < stages && k < turns; ++k) fetch(k);
-  float acc[NV][8], g[NV][8];
+  float2 acc[NV][4], g[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    load_gain(g[i], p.gain, p.g_dt, (i * tpr + t) * 8, p.cols, true);
+    float v[8];
+    load_gain(v, p.gain, p.g_dt, (i * tpr + t) * 8, p.cols, true);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      g[i][j] = make_float2(v[2 * j], v[2 * j + 1]);
+      acc[i][j] = make_float2(0.f, 0.f);
+    }
   }
   const float n = static_cast<float>(p.cols);
   for (int64_t k = 0; k < turns; ++k) {
@@ -441,7 +453,7 @@ __global__ void __launch_bounds__(256, 2)
     }
     if (__syncthreads_or(!ok)) break;      // every copy of this block lands before its memory is reused
     Chunk<WIDE> cd[NV], ch[NV], cs[NV];
-    float ss = 0.f, dot = 0.f;
+    float2 ss2 = make_float2(0.f, 0.f), dot2 = ss2;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * tpr + t) * 8;
@@ -449,43 +461,52 @@ __global__ void __launch_bounds__(256, 2)
       load_chunk<WIDE>(cd[i], d, p.dy_dt, col, p.cols, true);
       load_chunk<WIDE>(ch[i], d + bd, p.h_dt, col, p.cols, true);
       if (has_res) load_chunk<WIDE>(cs[i], d + bd + bh, p.dr_dt, col, p.cols, true);
-      float dv[8], h[8];
-      to_float<WIDE>(cd[i], p.dy_dt, dv);
-      to_float<WIDE>(ch[i], p.h_dt, h);
+      float2 dv[4], h[4];
+      to_float2<WIDE>(cd[i], p.dy_dt, dv);
+      to_float2<WIDE>(ch[i], p.h_dt, h);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ss = fmaf(h[j], h[j], ss);
-        dot = fmaf(dv[j] * g[i][j], h[j], dot);
+      for (int j = 0; j < 4; ++j) {
+        ss2 = ptx::fma2(h[j], h[j], ss2);
+        dot2 = ptx::fma2(ptx::mul2(dv[j], g[i][j]), h[j], dot2);
       }
     }
+    float ss = ss2.x + ss2.y, dot = dot2.x + dot2.y;
     row_reduce2(ss, dot, tpr, s_a[k & 1], s_b[k & 1]);
     if (t == 0 && k + stages < turns) fetch(k + stages);
     const float rstd = 1.f / sqrtf(ss / n + p.eps);
-    const float m = dot * rstd / n;
+    const float m = -rstd * rstd * (dot * rstd / n);
+    const float2 r2 = make_float2(rstd, rstd), m2 = make_float2(m, m);
     char* out = row_ptr(p.dh, p.dh_dt, blockIdx.x + k * slots, p.dhs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * tpr + t) * 8;
       if (col >= p.cols) continue;
-      float dv[8], h[8], r[8], o[8];
-      to_float<WIDE>(cd[i], p.dy_dt, dv);
-      to_float<WIDE>(ch[i], p.h_dt, h);
-      if (has_res) to_float<WIDE>(cs[i], p.dr_dt, r);
+      float2 dv[4], h[4], o[4];
+      to_float2<WIDE>(cd[i], p.dy_dt, dv);
+      to_float2<WIDE>(ch[i], p.h_dt, h);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = h[j] * rstd;
-        acc[i][j] = fmaf(dv[j], u, acc[i][j]);
-        o[j] = rstd * (dv[j] * g[i][j] - u * m) + (has_res ? r[j] : 0.f);
+      for (int j = 0; j < 4; ++j) o[j] = make_float2(0.f, 0.f);
+      if (has_res) to_float2<WIDE>(cs[i], p.dr_dt, o);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = ptx::fma2(ptx::mul2(dv[j], h[j]), r2, acc[i][j]);
+        // rstd gain dy - rstd u mean + dres, u = h rstd
+        o[j] = ptx::fma2(m2, h[j], ptx::fma2(r2, ptx::mul2(dv[j], g[i][j]), o[j]));
+        v[2 * j] = o[j].x;
+        v[2 * j + 1] = o[j].y;
       }
-      store_chunk(out, p.dh_dt, col, p.cols, true, o);
+      store_chunk(out, p.dh_dt, col, p.cols, true, v);
     }
   }
   if (p.part) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * tpr + t) * 8;
-      if (col < p.cols)
-        store_chunk(p.part + static_cast<int64_t>(blockIdx.x) * p.cols, kDtF32, col, p.cols, true, acc[i]);
+      if (col >= p.cols) continue;
+      const float v[8] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y,
+                          acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y};
+      store_chunk(p.part + static_cast<int64_t>(blockIdx.x) * p.cols, kDtF32, col, p.cols, true, v);
     }
   }
 }
@@ -494,6 +515,7 @@ __global__ void __launch_bounds__(256, 2)
 __global__ void __launch_bounds__(256) rmsnorm_dgain_kernel(const float* part, int slots, int cols,
                                                             float* dgain) {
   __shared__ float s[8][32];
+  ptx::wait_dependency();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31);
   const int g = threadIdx.x >> 5;
   float v = 0.f;
@@ -624,8 +646,7 @@ cudaError_t launch_norm_grad(const NormGradParams& p, int sms, cudaStream_t s) {
 }
 
 cudaError_t launch_norm_dgain(const float* part, int slots, int cols, float* dgain, cudaStream_t s) {
-  rmsnorm_dgain_kernel<<<(cols + 31) / 32, 256, 0, s>>>(part, slots, cols, dgain);
-  return cudaGetLastError();
+  return launch_after(rmsnorm_dgain_kernel, (cols + 31) / 32, 256, 0, s, part, slots, cols, dgain);
 }
 
 }  // namespace muon

@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "block.h"
+#include "sm100_ptx.cuh"
 
 namespace muon {
 
@@ -61,11 +62,12 @@ __device__ __forceinline__ bool load_logits(float (&x)[EPL], const void* base, i
 
 // Softmax parts: e[i] = exp(x[i] - max), returns their sum (0: every logit is -inf).
 template <int EPL>
-__device__ __forceinline__ float softmax_parts(const float (&x)[EPL], float (&e)[EPL]) {
+__device__ __forceinline__ float softmax_parts(const float (&x)[EPL], float (&e)[EPL], float* top) {
   float mx = x[0];
 #pragma unroll
   for (int i = 1; i < EPL; ++i) mx = fmaxf(mx, x[i]);
   mx = warp_max(mx);
+  *top = mx;
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
@@ -83,6 +85,7 @@ template <int EPL>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ RouteParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t tok = blockIdx.x * static_cast<int64_t>(kRouteWarps) + (threadIdx.x >> 5);
+  ptx::launch_dependents();
   if (tok >= p.tokens) return;
   const int k = p.top_k;
   int32_t my_idx = -1;
@@ -91,11 +94,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     float x[EPL], sc[EPL];
     if (load_logits<EPL>(x, p.logits, p.dtype, tok * p.stride, p.experts, lane))
       atomicOr(p.status, kDevNonfinite);
+    // every expert's score, where the choice goes by scores
+    const bool by_score = p.bias != nullptr || (p.top_groups < p.groups && p.group_score == 1);
+    float top = 0.f, sum = 0.f;
     if (p.score == 0) {
-      const float sum = softmax_parts<EPL>(x, sc);
+      sum = softmax_parts<EPL>(x, sc, &top);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) sc[i] = sum > 0.f ? sc[i] / sum : 0.f;
-    } else {
+    } else if (by_score) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) sc[i] = sigmoid(x[i]);
     }
@@ -204,15 +210,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
         rescan();
       }
     }
-    // the chosen experts' scores, from their lanes
-    for (int j = 0; j < k; ++j) {
-      const int e = __shfl_sync(kFull, my_idx, j);
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i == (e >> 5)) s = sc[i];
-      s = __shfl_sync(kFull, s, e & 31);
-      if (lane == j && e >= 0) my_score = s;
+    // the chosen experts' scores, each in its lane, from the logit again (in L1)
+    if (my_idx >= 0) {
+      const int64_t at = tok * p.stride + my_idx;
+      const float v = p.dtype == kDtF32 ? static_cast<const float*>(p.logits)[at]
+                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[at]);
+      my_score = p.score == 0 ? expf(v - top) / sum : sigmoid(v);
     }
   }
   if (p.renorm) {
@@ -234,7 +237,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   float x[EPL], sc[EPL], d[EPL];
   load_logits<EPL>(x, p.logits, p.dtype, tok * p.stride, p.experts, lane);
   if (p.score == 0) {
-    const float sum = softmax_parts<EPL>(x, sc);
+    float top;
+    const float sum = softmax_parts<EPL>(x, sc, &top);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sc[i] *= inv;
@@ -312,6 +316,8 @@ __device__ __forceinline__ int expert_of(const PlanParams& p, int64_t entry, int
 // hist[tile][e]: entries of expert e among the tile's tokens.
 __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(const __grid_constant__ PlanParams p) {
   extern __shared__ int s_cnt[];
+  ptx::launch_dependents();
+  ptx::wait_dependency();
   for (int e = threadIdx.x; e < p.experts; e += kPlanThreads) s_cnt[e] = 0;
   __syncthreads();
   const int64_t total = p.tokens * p.top_k;
@@ -340,6 +346,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   const int64_t first = blockIdx.x * static_cast<int64_t>(kPlanTokens) * p.top_k;
   const int64_t end = min(first + static_cast<int64_t>(kPlanTokens) * p.top_k, total);
   for (int i = threadIdx.x; i < kPlanWarps * E; i += kPlanThreads) start[i] = 0;
+  ptx::wait_dependency();
   __syncthreads();
   // this tile's counts per warp
   const int64_t run = (end - first + kPlanWarps * 32 - 1) / (kPlanWarps * 32) * 32;
@@ -358,10 +365,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       if (p.tiles == 1) {
         for (int w = 0; w < kPlanWarps; ++w) all += start[w * E + e];
       } else {
-        for (int b = 0; b < p.tiles; ++b) {
-          const int c = p.hist[static_cast<int64_t>(b) * E + e];
-          all += c;
-          if (b < static_cast<int>(blockIdx.x)) before += c;
+        for (int b0 = 0; b0 < p.tiles; b0 += 16) {      // 16 loads in flight
+          int c[16];
+#pragma unroll
+          for (int b = 0; b < 16; ++b)
+            c[b] = b0 + b < p.tiles ? p.hist[static_cast<int64_t>(b0 + b) * E + e] : 0;
+#pragma unroll
+          for (int b = 0; b < 16; ++b) {
+            all += c[b];
+            if (b0 + b < static_cast<int>(blockIdx.x)) before += c[b];
+          }
         }
       }
     }
@@ -446,14 +459,18 @@ cudaError_t launch_route_grad(const RouteGradParams& p, cudaStream_t s) {
   });
 }
 
-cudaError_t launch_plan_hist(const PlanParams& p, cudaStream_t s) {
-  plan_hist_kernel<<<p.tiles, kPlanThreads, p.experts * sizeof(int), s>>>(p);
+cudaError_t launch_plan_hist(const PlanParams& p, bool after, cudaStream_t s) {
+  const size_t smem = p.experts * sizeof(int);
+  if (after) return launch_after(plan_hist_kernel, p.tiles, kPlanThreads, smem, s, p);
+  plan_hist_kernel<<<p.tiles, kPlanThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_plan(const PlanParams& p, cudaStream_t s) {
+cudaError_t launch_plan(const PlanParams& p, bool after, cudaStream_t s) {
   // at most (8 + 1) * 1024 counters: 36 KB, under the default limit
-  plan_kernel<<<p.tiles, kPlanThreads, (kPlanWarps + 1) * p.experts * sizeof(int), s>>>(p);
+  const size_t smem = (kPlanWarps + 1) * p.experts * sizeof(int);
+  if (after) return launch_after(plan_kernel, p.tiles, kPlanThreads, smem, s, p);
+  plan_kernel<<<p.tiles, kPlanThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
