@@ -27,12 +27,16 @@ int api_device(ApiDevice* out);                                          // muon
 int api_workspace(cudaStream_t stream, size_t bytes, char** out);        // muon_status_t
 void api_set_launches(int n);
 
-// Launch of a kernel that follows another of the same call: it may start while
-// that one ends (programmatic dependent launch), and waits for its results
-// with ptx::wait_dependency before it touches what the call's kernels share.
+// Launch of a kernel that follows another of the same call.  early: it may
+// start while that one ends (programmatic dependent launch), and waits for its
+// results with ptx::wait_dependency before it touches what the call's kernels
+// share.  That saves 2 to 3 us a launch where the kernels are short (one token
+// through the experts' products 26.8 -> 21.3 us); under long ones the waiting
+// blocks take room from the running ones (the products' gradient over 64
+// experts 1247 -> 1266 us).
 template <typename... A>
-cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
-                         typename std::common_type<A>::type... args) {
+cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned block, size_t smem, bool early,
+                         cudaStream_t s, typename std::common_type<A>::type... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
@@ -42,7 +46,7 @@ cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned block, si
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -60,7 +64,7 @@ struct NormParams {
   int64_t rows, xs, rs, hs, ys;
   int cols;
   int x_dt, r_dt, g_dt, h_dt, y_dt;   // kDt*; kDtNone: absent
-  int group_chunks;                   // e4m3: 8-column chunks per scale, 0 = the whole row
+  int grouped;                        // e4m3: a scale per 128 columns (0: per row)
   int n_scales;                       // scales per row
   int vec;                            // 16-byte accesses are legal
   float eps;
@@ -129,9 +133,8 @@ struct PlanParams {
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t s);
 cudaError_t launch_route_grad(const RouteGradParams& p, cudaStream_t s);
-// after: the launch follows another of the same call (launch_after)
-cudaError_t launch_plan_hist(const PlanParams& p, bool after, cudaStream_t s);
-cudaError_t launch_plan(const PlanParams& p, bool after, cudaStream_t s);
+cudaError_t launch_plan_hist(const PlanParams& p, cudaStream_t s);
+cudaError_t launch_plan(const PlanParams& p, bool early, cudaStream_t s);   // early: see launch_after
 
 // ---- experts' products ---------------------------------------------------------------------
 // Products on the tensor cores (experts.cu), by operand and result.
@@ -153,6 +156,8 @@ struct ExGemmParams {
   const int32_t* offsets;         // [experts + 1]
   int64_t rows;                   // tokens * top_k, the most rows there are
   int experts;
+  int e0, e1;                     // experts of this launch (kExDw*: all)
+  int beside;                     // 1: runs beside the previous launch, whose results it does not use
   int pad;                        // padded row numbering: segments of 1 or kExSeg rows
   int m_tiles, n_tiles;           // M tiles of a pair; kExDw*: N tiles
   int kb;                         // K blocks of 64 (kExDw*: from the expert's rows)
@@ -168,7 +173,7 @@ struct ExGemmParams {
   int64_t yep;
   const float* wr;                // [padded rows] weight of a row
   __nv_bfloat16* dgu;             // [padded rows][gp], gate part then up part at ip
-  float* part;                    // [m_tiles * 8][rows] parts of dweights
+  float* part;                    // [features / 32][rows] parts of dweights
   void* dw;
   int dw_dt, dw_vec;
   int stages;                     // ring depth (set at the launch)
@@ -177,18 +182,18 @@ struct ExGemmParams {
   unsigned long long timeout_ns;
 };
 
-// Rows of x (and dout) in expert order, zero rows up to each segment's end.
+// Rows of x (or dout) of experts [e0, e1) in expert order, zero rows up to each segment's end.
 struct ExGatherParams {
-  const __nv_bfloat16* x[2];      // x, dout or null
-  int64_t xs[2];
-  __nv_bfloat16* out[2];          // [padded rows][hp]
+  const __nv_bfloat16* x;
+  int64_t xs;
+  __nv_bfloat16* out;             // [padded rows][hp]
   int vec;                        // 16-byte accesses are legal
   const float* weights;           // with wr: the row's weight
   float* wr;
   const int32_t* offsets;
   const int32_t* src;
   int64_t rows, hidden, hp;
-  int experts, top_k, pad;
+  int experts, top_k, pad, e0, e1;
 };
 
 struct ExCombineParams {          // out[t] = sum_j w[t,j] y[pos[t,j]]
@@ -231,9 +236,10 @@ struct ExFewParams {
 };
 cudaError_t launch_ex_few(const ExFewParams& p, cudaStream_t s);    // two launches
 
-cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, cudaStream_t s);
-cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, cudaStream_t s);
-cudaError_t launch_ex_combine(const ExCombineParams& p, int sms, cudaStream_t s);
+// early: see launch_after
+cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, bool early, cudaStream_t s);
+cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, int blocks, cudaStream_t s);
+cudaError_t launch_ex_combine(const ExCombineParams& p, int sms, bool early, cudaStream_t s);
 cudaError_t launch_ex_dweights(const ExWeightParams& p, cudaStream_t s);
 // mats matrices [rows][cols] -> [rows_p][cols_p], zeros around
 cudaError_t launch_ex_repack(const __nv_bfloat16* in, int64_t mats, int64_t rows, int64_t cols,

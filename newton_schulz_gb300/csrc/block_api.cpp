@@ -95,7 +95,7 @@ muon_status_t norm_impl(const muon_rmsnorm_t* a, cudaStream_t stream) {
   p.g_dt = a->gain ? a->gain_dtype : kDtNone;
   p.h_dt = a->h ? a->h_dtype : kDtNone;
   p.y_dt = a->y_dtype;
-  p.group_chunks = a->group / 8;
+  p.grouped = a->group != 0;
   p.n_scales = static_cast<int>(n_scales);
   p.eps = a->eps;
   p.vec = x.rows16() && r.rows16() && h.rows16() && y.rows16() && g.rows16();
@@ -182,8 +182,8 @@ bool unsupported_route(int64_t tokens, int top_k, int experts, int groups) {
 
 // The plan's launches; hist: workspace, unused with one tile.
 muon_status_t plan_launches(const PlanParams& p, Counter* c, cudaStream_t stream) {
-  if (p.tiles > 1) MUON_TRY(c->run(launch_plan_hist(p, c->n > 0, stream)));
-  return c->run(launch_plan(p, c->n > 0, stream));
+  if (p.tiles > 1) MUON_TRY(c->run(launch_plan_hist(p, stream)));
+  return c->run(launch_plan(p, c->n > 0 && p.tiles == 1, stream));
 }
 
 PlanParams plan_params(const int32_t* idx, int64_t tokens, int top_k, int experts, int32_t* offsets,
@@ -443,6 +443,7 @@ ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const Api
   p.offsets = a->offsets;
   p.rows = a->tokens * a->top_k;
   p.experts = a->experts;
+  p.e0 = 0, p.e1 = a->experts;
   p.pad = pad;
   p.inner = static_cast<int>(a->inner), p.ip = static_cast<int>(w.ip);
   p.ap = p.ip, p.gp = 2 * p.ip;
@@ -453,7 +454,8 @@ ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const Api
 ExGatherParams gather_params(const muon_experts_t* a, const WeightPlan& w, int pad) {
   ExGatherParams g;
   std::memset(&g, 0, sizeof(g));
-  g.x[0] = static_cast<const __nv_bfloat16*>(a->x), g.xs[0] = a->x_stride;
+  g.x = static_cast<const __nv_bfloat16*>(a->x), g.xs = a->x_stride;
+  g.e0 = 0, g.e1 = a->experts;
   g.offsets = a->offsets, g.src = a->src;
   g.rows = a->tokens * a->top_k, g.hidden = a->hidden, g.hp = w.hp;
   g.experts = a->experts, g.top_k = a->top_k, g.pad = pad;
@@ -486,7 +488,19 @@ struct RowPlan {
   }
 };
 
+constexpr int kGatherBlocks = 5;      // per SM, for a copy that runs alone
+constexpr int64_t kBesideRows = 16384;      // from here a copy takes longer than its overlap costs
+
 int tiles_of(int64_t n, int64_t per) { return static_cast<int>((n + per - 1) / per); }
+
+// Many rows: the copy of the first experts' rows runs alone, that of the rest
+// while the first experts' product runs (the copy needs HBM, the product the
+// tensor cores; one block an SM leaves it room).  The number of experts in the
+// first part, or 0: one copy, one product.  16384 tokens over 256 experts of
+// [768, 2048]: 1265 -> 1220 us.
+int beside_part(const muon_experts_t* a) {
+  return a->tokens * a->top_k >= kBesideRows && a->experts >= 8 ? a->experts / 3 : 0;
+}
 
 muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, void* gu, cudaStream_t stream) {
   ExpertsViews v;
@@ -536,10 +550,17 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   __nv_bfloat16* act = reinterpret_cast<__nv_bfloat16*>(ws + at_act);
   const __nv_bfloat16 *w_in, *w_out;
   MUON_TRY(pack_weights(a, w, ws, &w_in, &w_out, &c, stream));
+  const bool early = rows <= 4096;      // short kernels
   ExGatherParams g = gather_params(a, w, 1);
-  g.out[0] = xp;
+  g.out = xp;
   g.vec = v.x.rows16();
-  MUON_TRY(c.run(launch_ex_gather(g, rows, stream)));
+  const int part = beside_part(a);
+  if (part) {
+    g.e1 = part;
+    MUON_TRY(c.run(launch_ex_gather(g, rows, kGatherBlocks * d.sms, stream)));
+    g.e0 = part, g.e1 = a->experts;
+  }
+  MUON_TRY(c.run(launch_ex_gather(g, rows, (part ? 1 : kGatherBlocks) * d.sms, stream)));
   ExGemmParams up = gemm_params(a, w, d, 1);
   up.m_tiles = tiles_of(2 * w.ip, kExMTile), up.kb = tiles_of(H, 64), up.m = up.inner;
   up.act = act;
@@ -551,9 +572,14 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   if (!map_up(&up.mapA, w_in, a, w) || !map_rows(&up, xp, H, rows, w.hp) ||
       !map3(&down.mapA, w_out, I, H, a->experts, w.ip, 128) || !map_rows(&down, act, I, rows, w.ip))
     return MUON_ERR_CUDA;
-  MUON_TRY(c.run(launch_ex_gemm(kExUp, up, d.sms, stream)));
-  MUON_TRY(c.run(launch_ex_gemm(kExDown, down, d.sms, stream)));
-  MUON_TRY(c.run(launch_ex_combine(combine_params(a, down, a->weights, o), d.sms, stream)));
+  if (part) {
+    up.e1 = part, up.beside = 1;
+    MUON_TRY(c.run(launch_ex_gemm(kExUp, up, d.sms, true, stream)));
+    up.e0 = part, up.e1 = a->experts, up.beside = 0;
+  }
+  MUON_TRY(c.run(launch_ex_gemm(kExUp, up, d.sms, early, stream)));
+  MUON_TRY(c.run(launch_ex_gemm(kExDown, down, d.sms, early, stream)));
+  MUON_TRY(c.run(launch_ex_combine(combine_params(a, down, a->weights, o), d.sms, early, stream)));
   api_set_launches(c.n);
   return MUON_OK;
 }
@@ -589,7 +615,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   const RowPlan rp(dx ? rows : 0, H, &cv);
   // padded rows: every expert with rows adds at most kExSeg - 1
   const int64_t prows = rows + (kExSeg - 1) * std::min<int64_t>(a->experts, rows);
-  const int parts = tiles_of(I, kExMTile) * 8;
+  const int parts = tiles_of(I, 128) * 4;
   // pitches of whole 64-column chunks (map_mn); the columns past the data
   // reach only results that are not stored
   const int64_t xpitch = rup(H, 64), gpitch = rup(2 * w.ip, 64), apitch = rup(w.ip, 64);
@@ -606,14 +632,12 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   const __nv_bfloat16 *w_in, *w_out;
   MUON_TRY(pack_weights(a, w, ws, &w_in, &w_out, &c, stream));
   ExGatherParams g = gather_params(a, w, kExSeg);
-  if (!dw_in) g.x[0] = nullptr;
-  g.out[0] = xp;
-  g.x[1] = static_cast<const __nv_bfloat16*>(dout), g.xs[1] = dos, g.out[1] = dop;
+  g.hp = xpitch;
+  g.x = static_cast<const __nv_bfloat16*>(dout), g.xs = dos, g.out = dop;
+  g.vec = vd.rows16();
   g.weights = a->weights;
   g.wr = reinterpret_cast<float*>(ws + at_wr);
-  g.hp = xpitch;
-  g.vec = v.x.rows16() && vd.rows16();
-  MUON_TRY(c.run(launch_ex_gather(g, prows, stream)));
+  MUON_TRY(c.run(launch_ex_gather(g, prows, kGatherBlocks * d.sms, stream)));
   ExGemmParams da = gemm_params(a, w, d, kExSeg);
   da.m_tiles = tiles_of(I, kExMTile), da.kb = tiles_of(H, 64), da.m = da.inner;
   da.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));
@@ -623,19 +647,28 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   da.part = reinterpret_cast<float*>(ws + at_part);
   if (!map_weights_mn(&da, w_out, I, H, w.ip) || !map_rows(&da, dop, H, prows, xpitch))
     return MUON_ERR_CUDA;
-  MUON_TRY(c.run(launch_ex_gemm(kExDact, da, d.sms, stream)));
+  MUON_TRY(c.run(launch_ex_gemm(kExDact, da, d.sms, false, stream)));
   if (dweights) {
     const ExWeightParams wp{da.part, a->pos, dweights, rows, parts};
     MUON_TRY(c.run(launch_ex_dweights(wp, stream)));
   }
+  // x's rows, for dw_in: with many rows their copy runs beside dx's product
+  const bool beside = dx && dw_in && rows >= kBesideRows;
+  if (dw_in) {
+    g.x = static_cast<const __nv_bfloat16*>(a->x), g.xs = a->x_stride, g.out = xp;
+    g.vec = v.x.rows16();
+    g.wr = nullptr;
+    MUON_TRY(c.run(launch_ex_gather(g, prows, (beside ? 1 : kGatherBlocks) * d.sms, stream)));
+  }
   if (dx) {
     ExGemmParams p = gemm_params(a, w, d, kExSeg);
+    p.beside = beside;
     p.m_tiles = tiles_of(H, kExMTile), p.kb = tiles_of(2 * w.ip, 64), p.m = static_cast<int>(H);
     rp.set(&p, ws);
     if (!map_weights_mn(&p, w_in, H, 2 * w.ip, w.hp) || !map_rows(&p, dgu, 2 * w.ip, prows, gpitch))
       return MUON_ERR_CUDA;
-    MUON_TRY(c.run(launch_ex_gemm(kExDx, p, d.sms, stream)));
-    MUON_TRY(c.run(launch_ex_combine(combine_params(a, p, nullptr, ox), d.sms, stream)));
+    MUON_TRY(c.run(launch_ex_gemm(kExDx, p, d.sms, beside, stream)));
+    MUON_TRY(c.run(launch_ex_combine(combine_params(a, p, nullptr, ox), d.sms, false, stream)));
   }
   for (int k = 0; k < 2; ++k) {
     void* out = k ? dw_out : dw_in;
@@ -648,7 +681,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
     const int64_t ap = k ? xpitch : gpitch, bp = k ? apitch : xpitch;
     if (!map_mn(&p.mapA, k ? dop : dgu, ap, prows, ap, 0) || !map_mn(&p.mapB, k ? wact : xp, bp, prows, bp, 0))
       return MUON_ERR_CUDA;
-    MUON_TRY(c.run(launch_ex_gemm(k ? kExDwOut : kExDwIn, p, d.sms, stream)));
+    MUON_TRY(c.run(launch_ex_gemm(k ? kExDwOut : kExDwIn, p, d.sms, false, stream)));
   }
   api_set_launches(c.n);
   return MUON_OK;

@@ -59,6 +59,9 @@ constexpr int kMostStages = 6;
 constexpr int kBarBytes = 256;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kThreads = 320;
+// as for 480 threads: 136 registers, which leave room beside 10 warps for a
+// block of the row copy (two warps in each quarter of the SM)
+constexpr int kBoundThreads = 480;
 constexpr uint32_t kTmemCols = 512;
 constexpr unsigned kFull = 0xffffffffu;
 // least exponent of a piece of rows: its factors both ways are normal numbers
@@ -68,7 +71,9 @@ constexpr bool is_dw(int kind) { return kind == kExDwIn || kind == kExDwOut; }
 constexpr bool a_mn(int kind) { return kind >= kExDact; }   // A read MN-major
 
 // epilogue staging per set
-constexpr int set_bytes(int kind) { return is_dw(kind) ? 16 * 1024 : 12 * 1024; }
+constexpr int set_bytes(int kind) {
+  return is_dw(kind) ? 16 * 1024 : kind == kExDact ? 25 * 1024 : 12 * 1024;
+}
 int gemm_smem(int kind, int stages, int experts) {
   return stages * kStageBytes + 2 * set_bytes(kind) + kBarBytes + 3 * (experts + 1) * 4 + 1024;
 }
@@ -89,10 +94,12 @@ __device__ __forceinline__ void fetch_offsets(const Scan& s, const int32_t* offs
     s.off[e] = max(0, static_cast<int>(min(static_cast<int64_t>(offsets[e]), rows)));
 }
 
-__device__ __forceinline__ void scan_offsets(const Scan& s, int experts, int pad, bool tile_pads, int lane) {
+// Experts outside [e0, e1) get no row tiles.
+__device__ __forceinline__ void scan_offsets(const Scan& s, int experts, int pad, bool tile_pads, int e0, int e1,
+                                             int lane) {
   int top = 0, pbase = 0, tbase = 0;
-  for (int e0 = 0; e0 <= experts; e0 += 32) {
-    const int e = e0 + lane;
+  for (int eb = 0; eb <= experts; eb += 32) {
+    const int e = eb + lane;
     int v = e <= experts ? s.off[e] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -104,11 +111,11 @@ __device__ __forceinline__ void scan_offsets(const Scan& s, int experts, int pad
     top = __shfl_sync(kFull, v, 31);
   }
   __syncwarp();
-  for (int e0 = 0; e0 < experts; e0 += 32) {
-    const int e = e0 + lane;
+  for (int eb = 0; eb < experts; eb += 32) {
+    const int e = eb + lane;
     const int cnt = e < experts ? s.off[e + 1] - s.off[e] : 0;
     const int pc = round_up(cnt, pad);
-    const int nt = ((tile_pads ? pc : cnt) + kExNTile - 1) / kExNTile;
+    const int nt = e >= e0 && e < e1 ? ((tile_pads ? pc : cnt) + kExNTile - 1) / kExNTile : 0;
     int a = pc, b = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -389,92 +396,116 @@ __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, c
   }
 }
 
-// da -> dgu, w a and this warp's 32 features' part of <da, a>; 16 rows at a time
-__device__ __forceinline__ void epi_dact(const ExGemmParams& p, const Tile& t, const EpiWarp& w, int part) {
+// The tile's row weights into the set's staging, past the slabs.
+constexpr int kWeightOff = 24 * 1024;
+__device__ __forceinline__ void fetch_weights(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int row = w.tid + 128 * k;
+    const float v = row < t.valid ? p.wr[t.prow + row] : 0.f;
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(w.stg + kWeightOff + row * 4), "f"(v) : "memory");
+  }
+}
+
+// Gate and up rows of a slab of 32 rows, into registers: asked for a slab (and
+// a tile's first before its products are done) early, as their latency is
+// several slabs' arithmetic.
+struct GateUp {
+  uint4 v[8];     // rows tid / 16 + 8 k of the gates, then of the ups
+};
+__device__ __forceinline__ void fetch_gu(const ExGemmParams& p, const Tile& t, const EpiWarp& w, int c0,
+                                         GateUp& in) {
+  const int tok = w.tid >> 4, ft = w.m0 + (w.tid & 15) * 8;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int row = c0 + tok + 8 * (k & 3);
+    const __nv_bfloat16* q =
+        p.gu + static_cast<int64_t>(t.urow + row) * 2 * p.inner + (k >> 2) * p.inner + ft;
+    in.v[k] = load8(q, row < t.valid ? p.inner - ft : 0, p.gu_vec != 0);
+  }
+}
+
+// da -> dgu, w a and this warp's 32 features' part of <da, a>; 32 rows at a time
+__device__ __forceinline__ void epi_dact(const ExGemmParams& p, const Tile& t, const EpiWarp& w, GateUp& in) {
   const int tok = w.tid >> 4, chunk = w.tid & 15, ft = w.m0 + chunk * 8;
-  uint4 in[4];     // gate rows tok, tok + 8, then up rows
-  auto fetch = [&](int c0) {
+  constexpr uint32_t kUp = 8192, kAct = 16384;
+  for (int c0 = w.set * 32; c0 < t.rows; c0 += 64) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int row = c0 + tok + 8 * (k & 1);
-      const __nv_bfloat16* q =
-          p.gu + static_cast<int64_t>(t.urow + row) * 2 * p.inner + (k >> 1) * p.inner + ft;
-      in[k] = load8(q, row < t.valid ? p.inner - ft : 0, p.gu_vec != 0);
-    }
-  };
-  int c0 = w.set * 16;
-  if (c0 < t.rows) fetch(c0);
-  for (; c0 < t.rows; c0 += 32) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      sts16(staged(w.stg + (k >> 1) * 4096, tok + 8 * (k & 1), chunk, 256), in[k]);
-    if (c0 + 32 < t.rows) fetch(c0 + 32);
-    float wt[2][2], dot[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = c0 + 8 * i + 2 * (w.lane & 3) + j;
-        wt[i][j] = row < t.valid ? p.wr[t.prow + row] : 0.f;
-        dot[i][j] = 0.f;
-      }
+    for (int k = 0; k < 8; ++k)
+      sts16(staged(w.stg + (k >> 2) * kUp, tok + 8 * (k & 3), chunk, 256), in.v[k]);
+    if (c0 + 64 < t.rows) fetch_gu(p, t, w, c0 + 64, in);
     w.bar();
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint32_t r[8];
-      ptx::tmem_ld_16x256b_x2(w.taddr + (static_cast<uint32_t>(b * 16) << 16) + c0, r);
-      // matrix 2 i + c: rows 8 i.. of 8 features, chunk c of this 16-lane block
-      const int lr = (w.lane >> 4) * 8 + (w.lane & 7), lc = w.q4 * 4 + b * 2 + ((w.lane >> 3) & 1);
-      uint32_t g[4], u[4], a[4];
-      ptx::ldmatrix_x4_trans(staged(w.stg, lr, lc, 256), g);
-      ptx::ldmatrix_x4_trans(staged(w.stg + 4096, lr, lc, 256), u);
-      ptx::tmem_ld_wait();
+    for (int s = 0; s < 2; ++s) {       // 16 rows
+      const int cs = c0 + 16 * s;
+      float wt[2][2], dot[2][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t gv = g[2 * i + c], uv = u[2 * i + c];
-          float dg[2], du[2], wa[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float gg = j ? hi_of(gv) : lo_of(gv), uu = j ? hi_of(uv) : lo_of(uv);
-            const float da = f(r[4 * i + 2 * c + j]);
-            const float s = sigmoid(gg), sl = gg * s;
-            dot[i][j] = fmaf(da, sl * uu, dot[i][j]);
-            const float wd = wt[i][j] * da;
-            dg[j] = wd * uu * (s * (1.f + gg * (1.f - s)));
-            du[j] = wd * sl;
-            wa[j] = wt[i][j] * (sl * uu);
-          }
-          g[2 * i + c] = pack(dg[0], dg[1]);
-          u[2 * i + c] = pack(du[0], du[1]);
-          a[2 * i + c] = pack(wa[0], wa[1]);
+        for (int j = 0; j < 2; ++j) {
+          const int row = cs + 8 * i + 2 * (w.lane & 3) + j;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(wt[i][j]) : "r"(w.stg + kWeightOff + row * 4) : "memory");
+          dot[i][j] = 0.f;
         }
-      // a warp reads and writes its own four chunks only
-      ptx::stmatrix_x4_trans(staged(w.stg, lr, lc, 256), g);
-      ptx::stmatrix_x4_trans(staged(w.stg + 4096, lr, lc, 256), u);
-      ptx::stmatrix_x4_trans(staged(w.stg + 8192, lr, lc, 256), a);
-    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int b = 0; b < 2; ++b) {
+        uint32_t r[8];
+        ptx::tmem_ld_16x256b_x2(w.taddr + (static_cast<uint32_t>(b * 16) << 16) + cs, r);
+        // matrix 2 i + c: rows 8 i.. of 8 features, chunk c of this 16-lane block
+        const int lr = 16 * s + (w.lane >> 4) * 8 + (w.lane & 7);
+        const int lc = w.q4 * 4 + b * 2 + ((w.lane >> 3) & 1);
+        uint32_t g[4], u[4], a[4];
+        ptx::ldmatrix_x4_trans(staged(w.stg, lr, lc, 256), g);
+        ptx::ldmatrix_x4_trans(staged(w.stg + kUp, lr, lc, 256), u);
+        ptx::tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float v = dot[i][j];
-        v += __shfl_xor_sync(kFull, v, 4);
-        v += __shfl_xor_sync(kFull, v, 8);
-        v += __shfl_xor_sync(kFull, v, 16);
-        const int row = c0 + 8 * i + 2 * (w.lane & 3) + j;
-        if (w.lane < 4 && row < t.valid) p.part[(part + w.q4) * p.rows + t.urow + row] = v;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t gv = g[2 * i + c], uv = u[2 * i + c];
+            float dg[2], du[2], wa[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float gg = j ? hi_of(gv) : lo_of(gv), uu = j ? hi_of(uv) : lo_of(uv);
+              const float da = f(r[4 * i + 2 * c + j]);
+              const float sg = sigmoid(gg), sl = gg * sg;
+              dot[i][j] = fmaf(da, sl * uu, dot[i][j]);
+              const float wd = wt[i][j] * da;
+              dg[j] = wd * uu * (sg * (1.f + gg * (1.f - sg)));
+              du[j] = wd * sl;
+              wa[j] = wt[i][j] * (sl * uu);
+            }
+            g[2 * i + c] = pack(dg[0], dg[1]);
+            u[2 * i + c] = pack(du[0], du[1]);
+            a[2 * i + c] = pack(wa[0], wa[1]);
+          }
+        // a warp reads and writes its own four chunks only
+        ptx::stmatrix_x4_trans(staged(w.stg, lr, lc, 256), g);
+        ptx::stmatrix_x4_trans(staged(w.stg + kUp, lr, lc, 256), u);
+        ptx::stmatrix_x4_trans(staged(w.stg + kAct, lr, lc, 256), a);
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v = dot[i][j];
+          v += __shfl_xor_sync(kFull, v, 4);
+          v += __shfl_xor_sync(kFull, v, 8);
+          v += __shfl_xor_sync(kFull, v, 16);
+          const int row = cs + 8 * i + 2 * (w.lane & 3) + j;
+          if (w.lane < 4 && row < t.valid && w.m0 < p.m)
+            p.part[((w.m0 >> 5) + w.q4) * p.rows + t.urow + row] = v;
+        }
+    }
     w.bar();
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < 4; ++k) {
       const int row = tok + 8 * k;
       if (c0 + row >= t.rows) continue;
       const int64_t at = t.prow + c0 + row;
       store8(p.dgu + at * p.gp + ft, lds16(staged(w.stg, row, chunk, 256)), p.ip - ft, true);
-      store8(p.dgu + at * p.gp + p.ip + ft, lds16(staged(w.stg + 4096, row, chunk, 256)), p.ip - ft, true);
-      store8(p.act + at * p.ap + ft, lds16(staged(w.stg + 8192, row, chunk, 256)), p.ip - ft, true);
+      store8(p.dgu + at * p.gp + p.ip + ft, lds16(staged(w.stg + kUp, row, chunk, 256)), p.ip - ft, true);
+      store8(p.act + at * p.ap + ft, lds16(staged(w.stg + kAct, row, chunk, 256)), p.ip - ft, true);
     }
     w.bar();
   }
@@ -550,7 +581,7 @@ __device__ __forceinline__ void epi_dw(const ExGemmParams& p, const Tile& t, con
 }  // namespace
 
 template <int KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
     ex_gemm_kernel(const __grid_constant__ ExGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -594,13 +625,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) ptx::tmem_alloc_pair(tmem_slot, kTmemCols);
   fetch_offsets(scan, p.offsets, p.experts, p.rows);
   __syncthreads();
-  if (warp == 2) scan_offsets(scan, p.experts, p.pad, KIND == kExDact, lane);
+  if (warp == 2) scan_offsets(scan, p.experts, p.pad, KIND == kExDact, p.e0, p.e1, lane);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();     // both CTAs' barriers are initialised
   ptx::tc_fence_after();
   ptx::launch_dependents();
-  ptx::wait_dependency();
+  if (!p.beside) ptx::wait_dependency();
   const uint32_t tmem = *tmem_slot;
   const int tiles = is_dw(KIND) ? p.experts * p.m_tiles * p.n_tiles : scan.tt[p.experts] * p.m_tiles;
 
@@ -610,6 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool stop = false;
+      const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
       for (int tile = tile0; tile < tiles && !stop; tile += tstep) {
         const Tile t = decode<KIND>(p, scan, tile);
         // B: one box of 128 rows, or one or two of 32 for a small tile
@@ -622,7 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           if (crank == 0) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
-          const uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&full[stage]), 0);
+          const uint32_t bar = full0 + stage * 8;
           uint8_t* a = sStage + stage * kStageBytes;
           uint8_t* b = a + kOpBytes;
           const int k = i * BK;
@@ -667,6 +699,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0;
       bool stop = false;
+      const uint32_t s0 = ptx::smem_u32(sStage);
+      const uint64_t desc_a = a_mn(KIND) ? ptx::sdesc_mnmajor_sw128(s0, 8192, 1024) : ptx::sdesc_kmajor_sw128(s0);
+      const uint64_t desc_b = is_dw(KIND) ? ptx::sdesc_mnmajor_sw128(s0 + kOpBytes, 8192, 1024)
+                                          : ptx::sdesc_kmajor_sw128(s0 + kOpBytes);
+      const uint32_t a_lo = static_cast<uint32_t>(desc_a), b_lo = static_cast<uint32_t>(desc_b);
+      const uint64_t a_hi = desc_a >> 32 << 32, b_hi = desc_b >> 32 << 32;
       for (int tile = tile0; tile < tiles && !stop; tile += tstep) {
         const Tile t = decode<KIND>(p, scan, tile);
         if (t.kb == 0) continue;
@@ -677,21 +715,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + buf * 256;
+        uint32_t acc_on = 0;      // the tile's first MMA overwrites
         for (int i = 0; i < t.kb; ++i) {
           if (!wait_bounded(&full[stage], phase, abort_flag, p.status, p.timeout_ns, true)) {
             stop = true;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t a0 = ptx::smem_u32(sStage + stage * kStageBytes), b0 = a0 + kOpBytes;
+          // Addresses move in the descriptors' low word only (16-byte units),
+          // so a K block costs this thread a handful of additions: built anew,
+          // eight descriptors took longer than the MMAs they feed.
+          const uint32_t at = stage * (kStageBytes >> 4);
 #pragma unroll
           for (int k = 0; k < BK / UMMA_K; ++k) {
             // K-major: along the 128-byte row; MN-major: 16 rows (two 1024-byte atoms)
-            const uint64_t da = a_mn(KIND) ? ptx::sdesc_mnmajor_sw128(a0 + k * 2048, 8192, 1024)
-                                           : ptx::sdesc_kmajor_sw128(a0 + k * UMMA_K * 2);
-            const uint64_t db = is_dw(KIND) ? ptx::sdesc_mnmajor_sw128(b0 + k * 2048, 8192, 1024)
-                                            : ptx::sdesc_kmajor_sw128(b0 + k * UMMA_K * 2);
-            ptx::umma_bf16_pair(d, da, db, idesc, (i > 0 || k > 0) ? 1u : 0u);
+            const uint32_t da = a_lo + at + k * (a_mn(KIND) ? 2048 >> 4 : (UMMA_K * 2) >> 4);
+            const uint32_t db = b_lo + at + k * (is_dw(KIND) ? 2048 >> 4 : (UMMA_K * 2) >> 4);
+            ptx::umma_bf16_pair(d, a_hi | da, b_hi | db, idesc, acc_on);
+            acc_on = 1;
           }
           ptx::umma_commit_pair(&empty[stage], 0x3);
           if (++stage == kStages) {
@@ -721,6 +762,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       w.m0 = t.m * kExMTile + crank * 128;
       const int buf = acc & 1;
       w.taddr = tmem + buf * 256 + (static_cast<uint32_t>(w.q4 * 32) << 16);
+      GateUp in;
+      if (KIND == kExDact) {
+        fetch_weights(p, t, w);
+        if (w.set * 32 < t.rows) fetch_gu(p, t, w, w.set * 32, in);
+      }
       if (t.kb > 0) {
         wait_bounded(&tfull[buf], (acc >> 1) & 1, abort_flag, p.status, p.timeout_ns, false);
         // one decision for the set (its warps share a barrier); the slot
@@ -731,7 +777,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
       }
       if (KIND == kExUp) epi_up(p, t, w);
-      else if (KIND == kExDact) epi_dact(p, t, w, (t.m * 2 + crank) * 4);
+      else if (KIND == kExDact) epi_dact(p, t, w, in);
       else if (is_dw(KIND)) epi_dw<KIND>(p, t, w);
       else epi_rows(p, t, w);
       if (t.kb > 0) {
@@ -747,12 +793,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::cluster_sync();     // no copy, MMA or arrival still aims at the partner
   ptx::tc_fence_after();
   if (warp == 1) ptx::tmem_dealloc_pair(tmem, kTmemCols);
+  if (p.beside) ptx::wait_dependency();      // this kernel's end is also that one's
 }
 
-// Copies the rows of x (and dout) into expert order, a warp per row, four
+// Copies the rows of x (or dout) into expert order, a warp per row, eight
 // 16-byte loads a lane in flight and the next row's token with them; HBM-bound
 // (every row of x is read top_k times, from L2 while x fits there).
-__global__ void __launch_bounds__(256) ex_gather_kernel(const __grid_constant__ ExGatherParams p) {
+__global__ void __launch_bounds__(256, 5) ex_gather_kernel(const __grid_constant__ ExGatherParams p) {
   extern __shared__ int s_scan[];
   Scan s;
   s.off = s_scan;
@@ -762,9 +809,9 @@ __global__ void __launch_bounds__(256) ex_gather_kernel(const __grid_constant__ 
   ptx::launch_dependents();
   fetch_offsets(s, p.offsets, p.experts, p.rows);
   __syncthreads();
-  if (threadIdx.x < 32) scan_offsets(s, p.experts, p.pad, false, lane);
+  if (threadIdx.x < 32) scan_offsets(s, p.experts, p.pad, false, 0, 0, lane);
   __syncthreads();
-  const int total = s.poff[p.experts];
+  const int total = s.poff[p.e1];
   const int step = gridDim.x * 8;
   // token * top_k + slot of a padded row, -1 where there is none
   auto source = [&](int r) {
@@ -778,25 +825,24 @@ __global__ void __launch_bounds__(256) ex_gather_kernel(const __grid_constant__ 
     const int32_t v = p.src[urow];
     return v < p.rows ? v : -1;
   };
-  int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  int r = s.poff[p.e0] + blockIdx.x * 8 + (threadIdx.x >> 5);
   int sv = source(r);
   for (; r < total; r += step) {
     const int next = source(r + step);
     const int64_t tok = sv < 0 ? 0 : sv / p.top_k;
-    for (int q = 0; q < 2; ++q) {
-      if (!p.x[q]) continue;
-      const __nv_bfloat16* in = p.x[q] + tok * p.xs[q];
-      __nv_bfloat16* out = p.out[q] + r * p.hp;
-      for (int64_t c0 = lane * 8; c0 < p.hp; c0 += 1024) {
-        uint4 v[4];
+    {
+      const __nv_bfloat16* in = p.x + tok * p.xs;
+      __nv_bfloat16* out = p.out + r * p.hp;
+      for (int64_t c0 = lane * 8; c0 < p.hp; c0 += 2048) {
+        uint4 v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
           const int64_t c = c0 + 256 * j;
           v[j] = load8(in + c, sv < 0 ? 0 : static_cast<int>(min(p.hidden - c, static_cast<int64_t>(8))),
                        p.vec != 0);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 8; ++j)
           if (c0 + 256 * j < p.hp) *reinterpret_cast<uint4*>(out + c0 + 256 * j) = v[j];
       }
     }
@@ -895,47 +941,52 @@ __global__ void __launch_bounds__(256)
 namespace {
 
 template <int KIND>
-cudaError_t gemm_launch(ExGemmParams p, int sms, cudaStream_t s) {
+cudaError_t gemm_launch(ExGemmParams p, int sms, bool early, cudaStream_t s) {
   p.stages = kMostStages;
   if (gemm_smem(KIND, p.stages, p.experts) > kSmemLimit) p.stages = kMostStages - 1;
   const int smem = gemm_smem(KIND, p.stages, p.experts);
   const cudaError_t e = cudaFuncSetAttribute(ex_gemm_kernel<KIND>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_after(ex_gemm_kernel<KIND>, sms / 2 * 2, kThreads, smem, s, p);
+  return launch_after(ex_gemm_kernel<KIND>, sms / 2 * 2, kThreads, smem, early, s, p);
 }
 
 unsigned some(int64_t n, int64_t most) { return static_cast<unsigned>(std::min(std::max<int64_t>(n, 1), most)); }
 
 }  // namespace
 
-cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, cudaStream_t s) {
+cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, bool early, cudaStream_t s) {
   switch (kind) {
-    case kExUp: return gemm_launch<kExUp>(p, sms, s);
-    case kExDown: return gemm_launch<kExDown>(p, sms, s);
-    case kExDact: return gemm_launch<kExDact>(p, sms, s);
-    case kExDx: return gemm_launch<kExDx>(p, sms, s);
-    case kExDwIn: return gemm_launch<kExDwIn>(p, sms, s);
-    default: return gemm_launch<kExDwOut>(p, sms, s);
+    case kExUp: return gemm_launch<kExUp>(p, sms, early, s);
+    case kExDown: return gemm_launch<kExDown>(p, sms, early, s);
+    case kExDact: return gemm_launch<kExDact>(p, sms, early, s);
+    case kExDx: return gemm_launch<kExDx>(p, sms, early, s);
+    case kExDwIn: return gemm_launch<kExDwIn>(p, sms, early, s);
+    default: return gemm_launch<kExDwOut>(p, sms, early, s);
   }
 }
 
-cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, cudaStream_t s) {
-  ex_gather_kernel<<<some((padded_rows + 7) / 8, 1216), 256, 3 * (p.experts + 1) * sizeof(int), s>>>(p);
+cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, int blocks, cudaStream_t s) {
+  // the products' split of the SM's memory: an SM changes it only when idle, and
+  // a product is to start beside this kernel
+  const cudaError_t e = cudaFuncSetAttribute(ex_gather_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return e;
+  ex_gather_kernel<<<some((padded_rows + 7) / 8, blocks), 256, 3 * (p.experts + 1) * sizeof(int), s>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_ex_combine(const ExCombineParams& p, int sms, cudaStream_t s) {
+cudaError_t launch_ex_combine(const ExCombineParams& p, int sms, bool early, cudaStream_t s) {
   const unsigned warps = some((p.hidden + 255) / 256, 8), block = warps * 32;
   const unsigned grid = some(p.tokens, static_cast<int64_t>(sms) * (24 / warps));
-  if (p.top_k == 1) return launch_after(ex_combine_kernel<1>, grid, block, 0, s, p);
-  if (p.top_k == 2) return launch_after(ex_combine_kernel<2>, grid, block, 0, s, p);
-  if (p.top_k <= 4) return launch_after(ex_combine_kernel<4>, grid, block, 0, s, p);
-  return launch_after(ex_combine_kernel<8>, grid, block, 0, s, p);
+  if (p.top_k == 1) return launch_after(ex_combine_kernel<1>, grid, block, 0, early, s, p);
+  if (p.top_k == 2) return launch_after(ex_combine_kernel<2>, grid, block, 0, early, s, p);
+  if (p.top_k <= 4) return launch_after(ex_combine_kernel<4>, grid, block, 0, early, s, p);
+  return launch_after(ex_combine_kernel<8>, grid, block, 0, early, s, p);
 }
 
 cudaError_t launch_ex_dweights(const ExWeightParams& p, cudaStream_t s) {
-  return launch_after(ex_dweights_kernel, some((p.rows + 255) / 256, 1 << 16), 256, 0, s, p);
+  return launch_after(ex_dweights_kernel, some((p.rows + 255) / 256, 1 << 16), 256, 0, false, s, p);
 }
 
 cudaError_t launch_ex_repack(const __nv_bfloat16* in, int64_t mats, int64_t rows, int64_t cols,

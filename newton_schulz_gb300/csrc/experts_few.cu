@@ -61,9 +61,9 @@ __device__ __forceinline__ uint4 ld(const __nv_bfloat16* p) { return *reinterpre
 
 __global__ void __launch_bounds__(kWarps * 32) ex_few_up_kernel(const __grid_constant__ ExFewParams p) {
   const int lane = threadIdx.x & 31;
-  const int64_t u = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5);
+  const int u = blockIdx.x * kWarps + (threadIdx.x >> 5);      // rows * inner and tokens * hidden fit
   ptx::launch_dependents();
-  const int row = static_cast<int>(u / p.inner), ft = static_cast<int>(u - static_cast<int64_t>(row) * p.inner);
+  const int row = u / p.inner, ft = u - row * p.inner;
   if (row >= p.rows) return;
   Ends ends;
   ends.load(p.offsets, p.experts, lane);
@@ -115,9 +115,8 @@ __global__ void __launch_bounds__(kWarps * 32) ex_few_up_kernel(const __grid_con
 
 __global__ void __launch_bounds__(kWarps * 32) ex_few_down_kernel(const __grid_constant__ ExFewParams p) {
   const int lane = threadIdx.x & 31;
-  const int64_t u = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5);
-  const int64_t t = u / p.hidden;
-  const int h = static_cast<int>(u - t * p.hidden);
+  const int u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int t = u / p.hidden, h = u - t * p.hidden;
   if (t >= p.tokens) return;
   Ends ends;
   ends.load(p.offsets, p.experts, lane);
@@ -194,7 +193,7 @@ cudaError_t launch_ex_few(const ExFewParams& p, cudaStream_t s) {
   ex_few_up_kernel<<<static_cast<unsigned>(up), kWarps * 32, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_after(ex_few_down_kernel, static_cast<unsigned>(down), kWarps * 32, 0, s, p);
+  return launch_after(ex_few_down_kernel, static_cast<unsigned>(down), kWarps * 32, 0, true, s, p);
 }
 
 }  // namespace muon

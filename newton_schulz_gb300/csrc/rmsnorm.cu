@@ -192,6 +192,111 @@ __device__ __forceinline__ void row_reduce2(float& a, float& b, int tpr, float* 
 
 }  // namespace
 
+// One row from its loaded chunks: statistics, h, y.
+template <int NV, bool WIDE>
+__device__ __forceinline__ void norm_row(const NormParams& p, const Chunk<WIDE> (&cx)[NV],
+                                         const Chunk<WIDE> (&cr)[NV], int64_t row, bool live, int t, int tpr,
+                                         float* s_sum, float* s_max) {
+  const bool vec = p.vec != 0, has_res = p.r_dt != kDtNone;
+  // h of chunk i, recomputed where it is needed
+  auto sum = [&](int i, float2 (&v)[4]) {
+    if ((i * tpr + t) * 8 >= p.cols) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = make_float2(0.f, 0.f);
+      return;
+    }
+    to_float2<WIDE>(cx[i], p.x_dt, v);
+    if (has_res) {
+      float2 r[4];
+      to_float2<WIDE>(cr[i], p.r_dt, r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = ptx::add2(v[j], r[j]);
+    }
+  };
+  auto flat = [](const float2 (&v)[4], float (&o)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[2 * j] = v[j].x;
+      o[2 * j + 1] = v[j].y;
+    }
+  };
+  char* hr = p.h_dt != kDtNone ? row_ptr(p.h, p.h_dt, row, p.hs) : nullptr;
+  float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * tpr + t) * 8;
+    float2 v[4];
+    sum(i, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s2 = ptx::fma2(v[j], v[j], s2);
+    if (hr && live && col < p.cols) {
+      float o[8];
+      flat(v, o);
+      store_chunk(hr, p.h_dt, col, p.cols, vec, o);
+    }
+  }
+  const float ss = row_reduce<false>(s2.x + s2.y, tpr, s_sum);
+  const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.cols) + p.eps);
+  const float2 r2 = make_float2(rstd, rstd);
+  // gain * h * rstd of chunk i
+  auto scaled = [&](int i, float (&o)[8]) {
+    float2 v[4];
+    float g[8];
+    sum(i, v);
+    load_gain(g, p.gain, p.g_dt, (i * tpr + t) * 8, p.cols, vec);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = ptx::mul2(ptx::mul2(v[j], r2), make_float2(g[2 * j], g[2 * j + 1]));
+    flat(v, o);
+  };
+  char* yr = row_ptr(p.y, p.y_dt, row, p.ys);
+  const bool e4m3 = p.y_dt == kDtE4m3;
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = i * tpr + t, col = c * 8;
+    float v[8];
+    scaled(i, v);
+    if (!e4m3) {
+      if (live && col < p.cols) store_chunk(yr, p.y_dt, col, p.cols, vec, v);
+      continue;
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+    if (!p.grouped) {
+      top = fmaxf(top, m);
+      continue;
+    }
+    // 16 chunks (128 columns) lie in 16 consecutive lanes: tpr is a multiple of 16
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = fmaxf(m, 1e-12f);
+    if (live && col < p.cols) {
+      const float k = 448.f / m;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= k;
+      store_chunk(yr, kDtE4m3, col, p.cols, vec, v);
+      if ((c & 15) == 0) p.scales[row * p.n_scales + (c >> 4)] = m / 448.f;
+    }
+  }
+  if (!e4m3 || p.grouped) return;
+  // one scale for the row
+  top = fmaxf(row_reduce<true>(top, tpr, s_max), 1e-12f);
+  const float k = 448.f / top;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * tpr + t) * 8;
+    if (!live || col >= p.cols) continue;
+    float v[8];
+    scaled(i, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= k;
+    store_chunk(yr, kDtE4m3, col, p.cols, vec, v);
+    if (col == 0) p.scales[row] = top / 448.f;
+  }
+}
+
 template <int NV, bool WIDE>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 8 ? 512 : 256, NV == 2 ? 3 : NV == 4 ? (WIDE ? 2 : 3) : 1)
     rmsnorm_kernel(const __grid_constant__ NormParams p, int tpr) {
@@ -218,84 +323,23 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 8 ? 512 : 256, NV == 2 
       if (col < p.cols) load_chunk<WIDE>(cr[i], rr, p.r_dt, col, p.cols, vec);
     }
   }
-  // h of chunk i, recomputed where it is needed
-  auto sum = [&](int i, float (&v)[8]) {
-    if ((i * tpr + t) * 8 >= p.cols) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
-      return;
-    }
-    to_float<WIDE>(cx[i], p.x_dt, v);
-    if (has_res) {
-      float r[8];
-      to_float<WIDE>(cr[i], p.r_dt, r);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += r[j];
-    }
-  };
-  char* hr = p.h_dt != kDtNone ? row_ptr(p.h, p.h_dt, row, p.hs) : nullptr;
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = (i * tpr + t) * 8;
-    float v[8];
-    sum(i, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-    if (hr && live && col < p.cols) store_chunk(hr, p.h_dt, col, p.cols, vec, v);
+  norm_row<NV, WIDE>(p, cx, cr, row, live, t, tpr, s_sum, s_max);
+}
+
+// Bounded wait of a whole block on one of its ring's stages; false: gave up.
+__device__ __forceinline__ bool ring_wait(uint64_t* full, uint32_t parity, unsigned* status,
+                                          unsigned long long timeout_ns) {
+  const uint32_t bar = ptx::smem_u32(full);
+  bool ok = ptx::mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = ptx::globaltimer();
+    while (!(ok = ptx::mbar_try_wait(bar, parity)))
+      if (ptx::globaltimer() - t0 > timeout_ns) {
+        atomicOr(status, kDevTimeout);
+        break;
+      }
   }
-  ss = row_reduce<false>(ss, tpr, s_sum);
-  const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.cols) + p.eps);
-  char* yr = row_ptr(p.y, p.y_dt, row, p.ys);
-  const bool e4m3 = p.y_dt == kDtE4m3;
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = i * tpr + t, col = c * 8;
-    float v[8], g[8];
-    sum(i, v);
-    load_gain(g, p.gain, p.g_dt, col, p.cols, vec);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * g[j];
-    if (!e4m3) {
-      if (live && col < p.cols) store_chunk(yr, p.y_dt, col, p.cols, vec, v);
-      continue;
-    }
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-    if (p.group_chunks == 0) {
-      top = fmaxf(top, m);
-      continue;
-    }
-    // 16 chunks (128 columns) lie in 16 consecutive lanes: tpr is a multiple of 16
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    m = fmaxf(m, 1e-12f);
-    if (live && col < p.cols) {
-      const float k = 448.f / m;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= k;
-      store_chunk(yr, kDtE4m3, col, p.cols, vec, v);
-      if (c % p.group_chunks == 0) p.scales[row * p.n_scales + c / p.group_chunks] = m / 448.f;
-    }
-  }
-  if (!e4m3 || p.group_chunks != 0) return;
-  // one scale for the row
-  top = fmaxf(row_reduce<true>(top, tpr, s_max), 1e-12f);
-  const float k = 448.f / top;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = (i * tpr + t) * 8;
-    if (!live || col >= p.cols) continue;
-    float v[8], g[8];
-    sum(i, v);
-    load_gain(g, p.gain, p.g_dt, col, p.cols, vec);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * g[j] * k;
-    store_chunk(yr, kDtE4m3, col, p.cols, vec, v);
-    if (col == 0) p.scales[row] = top / 448.f;
-  }
+  return !__syncthreads_or(!ok);
 }
 
 // Gradient: row slot s takes rows s, s + slots, ...; its share of dgain stays
@@ -408,11 +452,8 @@ __global__ void __launch_bounds__(256, 2)
   const uint32_t bd = p.cols * (p.dy_dt == kDtF32 ? 4 : 2), bh = p.cols * (p.h_dt == kDtF32 ? 4 : 2),
                  bs = has_res ? p.cols * (p.dr_dt == kDtF32 ? 4 : 2) : 0, bytes = bd + bh + bs;
   const uint32_t pitch = (bytes + 127) / 128 * 128;
-  const int64_t slots = gridDim.x;
-  const int64_t turns = (p.rows - blockIdx.x + slots - 1) / slots;
-  auto fetch = [&](int64_t k) {
-    const int64_t row = blockIdx.x + k * slots;
-    const int s = static_cast<int>(k % stages);
+  const int step = gridDim.x, rows = static_cast<int>(p.rows);
+  auto fetch = [&](int64_t row, int s) {
     uint8_t* d = ring + s * pitch;
     ptx::mbar_arrive_expect_tx(&full[s], bytes);
     ptx::bulk_load(d, row_ptr(p.dy, p.dy_dt, row, p.dys), bd, &full[s]);
@@ -425,7 +466,8 @@ __global__ void __launch_bounds__(256, 2)
   }
   __syncthreads();
   if (t == 0)
-    for (int64_t k = 0; k < stages && k < turns; ++k) fetch(k);
+    for (int s = 0; s < stages; ++s)
+      if (blockIdx.x + static_cast<int64_t>(s) * step < rows) fetch(blockIdx.x + s * step, s);
   float2 acc[NV][4], g[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -438,20 +480,11 @@ __global__ void __launch_bounds__(256, 2)
     }
   }
   const float n = static_cast<float>(p.cols);
-  for (int64_t k = 0; k < turns; ++k) {
-    const int s = static_cast<int>(k % stages);
-    const uint32_t bar = ptx::smem_u32(&full[s]), parity = static_cast<uint32_t>((k / stages) & 1);
+  int s = 0, par = 0;
+  uint32_t phase = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += step) {
+    if (!ring_wait(&full[s], phase, p.status, p.timeout_ns)) break;
     const uint8_t* d = ring + s * pitch;
-    bool ok = ptx::mbar_try_wait(bar, parity);
-    if (!ok) {
-      const uint64_t t0 = ptx::globaltimer();
-      while (!(ok = ptx::mbar_try_wait(bar, parity)))
-        if (ptx::globaltimer() - t0 > p.timeout_ns) {
-          atomicOr(p.status, kDevTimeout);
-          break;
-        }
-    }
-    if (__syncthreads_or(!ok)) break;      // every copy of this block lands before its memory is reused
     Chunk<WIDE> cd[NV], ch[NV], cs[NV];
     float2 ss2 = make_float2(0.f, 0.f), dot2 = ss2;
 #pragma unroll
@@ -471,12 +504,18 @@ __global__ void __launch_bounds__(256, 2)
       }
     }
     float ss = ss2.x + ss2.y, dot = dot2.x + dot2.y;
-    row_reduce2(ss, dot, tpr, s_a[k & 1], s_b[k & 1]);
-    if (t == 0 && k + stages < turns) fetch(k + stages);
+    row_reduce2(ss, dot, tpr, s_a[par], s_b[par]);
+    const int64_t next = row + static_cast<int64_t>(stages) * step;
+    if (t == 0 && next < rows) fetch(next, s);
+    par ^= 1;
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
     const float rstd = 1.f / sqrtf(ss / n + p.eps);
     const float m = -rstd * rstd * (dot * rstd / n);
     const float2 r2 = make_float2(rstd, rstd), m2 = make_float2(m, m);
-    char* out = row_ptr(p.dh, p.dh_dt, blockIdx.x + k * slots, p.dhs);
+    char* out = row_ptr(p.dh, p.dh_dt, row, p.dhs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * tpr + t) * 8;
@@ -553,7 +592,9 @@ cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t s) {
   // flight a thread.
   const int chunks = (p.cols + 7) / 8;
   const bool wide = p.x_dt != kDtBf16 || (p.r_dt != kDtNone && p.r_dt != kDtBf16);
-  const int nv = p.rows <= 4 * sms && chunks <= 1024 ? 1 : wide && chunks <= 512 ? 2 : chunks <= 1024 ? 4 : 8;
+  const int nv = p.rows <= 4 * sms && chunks <= 1024 ? 1
+                 : wide && p.rows <= 64 * sms && chunks <= 256 ? 1
+                 : wide && chunks <= 512 ? 2 : chunks <= 1024 ? 4 : 8;
   const int tpr = threads_per_row(p.cols, nv, 16);
   const int block = tpr > 32 ? tpr : 128;
   const int64_t grid = (p.rows + block / tpr - 1) / (block / tpr);
@@ -646,7 +687,7 @@ cudaError_t launch_norm_grad(const NormGradParams& p, int sms, cudaStream_t s) {
 }
 
 cudaError_t launch_norm_dgain(const float* part, int slots, int cols, float* dgain, cudaStream_t s) {
-  return launch_after(rmsnorm_dgain_kernel, (cols + 31) / 32, 256, 0, s, part, slots, cols, dgain);
+  return launch_after(rmsnorm_dgain_kernel, (cols + 31) / 32, 256, 0, true, s, part, slots, cols, dgain);
 }
 
 }  // namespace muon

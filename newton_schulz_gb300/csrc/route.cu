@@ -316,8 +316,6 @@ __device__ __forceinline__ int expert_of(const PlanParams& p, int64_t entry, int
 // hist[tile][e]: entries of expert e among the tile's tokens.
 __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(const __grid_constant__ PlanParams p) {
   extern __shared__ int s_cnt[];
-  ptx::launch_dependents();
-  ptx::wait_dependency();
   for (int e = threadIdx.x; e < p.experts; e += kPlanThreads) s_cnt[e] = 0;
   __syncthreads();
   const int64_t total = p.tokens * p.top_k;
@@ -459,19 +457,14 @@ cudaError_t launch_route_grad(const RouteGradParams& p, cudaStream_t s) {
   });
 }
 
-cudaError_t launch_plan_hist(const PlanParams& p, bool after, cudaStream_t s) {
-  const size_t smem = p.experts * sizeof(int);
-  if (after) return launch_after(plan_hist_kernel, p.tiles, kPlanThreads, smem, s, p);
-  plan_hist_kernel<<<p.tiles, kPlanThreads, smem, s>>>(p);
+cudaError_t launch_plan_hist(const PlanParams& p, cudaStream_t s) {
+  plan_hist_kernel<<<p.tiles, kPlanThreads, p.experts * sizeof(int), s>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_plan(const PlanParams& p, bool after, cudaStream_t s) {
+cudaError_t launch_plan(const PlanParams& p, bool early, cudaStream_t s) {
   // at most (8 + 1) * 1024 counters: 36 KB, under the default limit
-  const size_t smem = (kPlanWarps + 1) * p.experts * sizeof(int);
-  if (after) return launch_after(plan_kernel, p.tiles, kPlanThreads, smem, s, p);
-  plan_kernel<<<p.tiles, kPlanThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(plan_kernel, p.tiles, kPlanThreads, (kPlanWarps + 1) * p.experts * sizeof(int), early, s, p);
 }
 
 }  // namespace muon
