@@ -202,6 +202,34 @@ __device__ __forceinline__ Tile decode(const ExGemmParams& p, const Scan& s, int
   return t;
 }
 
+// A warp's tiles in order, decoded 32 at a time, one by each lane: decoding (a
+// search of the offsets and four divisions, about 1200 cycles) once per tile in
+// the copies' and the MMAs' threads cost a fifth of a tile of 12 K blocks.
+template <int KIND>
+struct Feed {
+  Tile mine;
+  // tile `it` of this pair; every lane calls it with the same `it`, in order
+  __device__ __forceinline__ Tile get(const ExGemmParams& p, const Scan& s, int tiles, int tile0, int tstep,
+                                      int it, int lane) {
+    if ((it & 31) == 0) {
+      const int64_t tile = tile0 + static_cast<int64_t>(it + lane) * tstep;
+      if (tile < tiles) mine = decode<KIND>(p, s, static_cast<int>(tile));
+    }
+    Tile t;
+    const int from = it & 31;
+    t.e = __shfl_sync(kFull, mine.e, from);
+    t.m = __shfl_sync(kFull, mine.m, from);
+    t.n = __shfl_sync(kFull, mine.n, from);
+    t.prow = __shfl_sync(kFull, mine.prow, from);
+    t.urow = __shfl_sync(kFull, mine.urow, from);
+    t.rows = __shfl_sync(kFull, mine.rows, from);
+    t.valid = __shfl_sync(kFull, mine.valid, from);
+    t.cols = __shfl_sync(kFull, mine.cols, from);
+    t.kb = __shfl_sync(kFull, mine.kb, from);
+    return t;
+  }
+};
+
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                              unsigned* status, unsigned long long timeout_ns,
                                              bool honour_abort) {
@@ -636,66 +664,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
   const int tiles = is_dw(KIND) ? p.experts * p.m_tiles * p.n_tiles : scan.tt[p.experts] * p.m_tiles;
 
   if (warp == 0) {
-    // ---- TMA producer -------------------------------------------------------------------
-    if (lane == 0) {
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      bool stop = false;
-      const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
-      for (int tile = tile0; tile < tiles && !stop; tile += tstep) {
-        const Tile t = decode<KIND>(p, scan, tile);
-        // B: one box of 128 rows, or one or two of 32 for a small tile
-        const int half = t.cols / 2, boxes = half > 64 ? 0 : (half + 31) / 32;
-        const uint32_t bytes = 2 * (kOpBytes + (boxes ? boxes * 4096 : kOpBytes));
-        const int m0 = t.m * kExMTile + crank * 128;
-        for (int i = 0; i < t.kb; ++i) {
-          if (!wait_bounded(&empty[stage], phase ^ 1, abort_flag, p.status, p.timeout_ns, true)) {
-            stop = true;
-            break;
-          }
-          if (crank == 0) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
-          const uint32_t bar = full0 + stage * 8;
-          uint8_t* a = sStage + stage * kStageBytes;
-          uint8_t* b = a + kOpBytes;
-          const int k = i * BK;
-          if (KIND == kExUp) {
-            // 8 features x (gate, up) x 8 groups: 128 rows
-            ptx::tma_load_5d_pair(a, &p.mapA, bar, k, 0, 0, m0 >> 4, t.e);
-          } else if (KIND == kExDown) {
-            ptx::tma_load_3d_pair(a, &p.mapA, bar, k, m0, t.e);
-          } else if (is_dw(KIND)) {
-            ptx::tma_load_3d_pair(a, &p.mapA, bar, 0, t.prow + k, m0 / 64);
-          } else if (p.a_whole) {
-            ptx::tma_load_4d_pair(a, &p.mapA, bar, 0, k, m0 / 64, t.e);
-          } else {
+    // ---- TMA producer (lane 0; the others hold tiles) -----------------------------------
+    Feed<KIND> feed;
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool stop = false;
+    const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
+    for (int tile = tile0, it = 0; tile < tiles && !stop; tile += tstep, ++it) {
+      const Tile t = feed.get(p, scan, tiles, tile0, tstep, it, lane);
+      // B: one box of 128 rows, or one or two of 32 for a small tile
+      const int half = t.cols / 2, boxes = half > 64 ? 0 : (half + 31) / 32;
+      const uint32_t bytes = 2 * (kOpBytes + (boxes ? boxes * 4096 : kOpBytes));
+      const int m0 = t.m * kExMTile + crank * 128;
+      for (int i = 0; lane == 0 && i < t.kb; ++i) {
+        if (!wait_bounded(&empty[stage], phase ^ 1, abort_flag, p.status, p.timeout_ns, true)) {
+          stop = true;
+          break;
+        }
+        if (crank == 0) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
+        const uint32_t bar = full0 + stage * 8;
+        uint8_t* a = sStage + stage * kStageBytes;
+        uint8_t* b = a + kOpBytes;
+        const int k = i * BK;
+        if (KIND == kExUp) {
+          // 8 features x (gate, up) x 8 groups: 128 rows
+          ptx::tma_load_5d_pair(a, &p.mapA, bar, k, 0, 0, m0 >> 4, t.e);
+        } else if (KIND == kExDown) {
+          ptx::tma_load_3d_pair(a, &p.mapA, bar, k, m0, t.e);
+        } else if (is_dw(KIND)) {
+          ptx::tma_load_3d_pair(a, &p.mapA, bar, 0, t.prow + k, m0 / 64);
+        } else if (p.a_whole) {
+          ptx::tma_load_4d_pair(a, &p.mapA, bar, 0, k, m0 / 64, t.e);
+        } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              ptx::tma_load_3d_pair(a + h * 8192, &p.mapA, bar, m0 + 64 * h, k, t.e);
-          }
-          if (is_dw(KIND)) {
-            ptx::tma_load_3d_pair(b, &p.mapB, bar, 0, t.prow + k, t.n * 4 + crank * 2);
-          } else if (boxes == 0) {
-            ptx::tma_load_2d_pair(b, &p.mapB, bar, k, t.prow + crank * half);
-          } else {
-            for (int h = 0; h < boxes; ++h)
-              ptx::tma_load_2d_pair(b + h * 4096, &p.mapB32, bar, k, t.prow + crank * half + 32 * h);
-          }
-          ++issued;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+          for (int h = 0; h < 2; ++h)
+            ptx::tma_load_3d_pair(a + h * 8192, &p.mapA, bar, m0 + 64 * h, k, t.e);
+        }
+        if (is_dw(KIND)) {
+          ptx::tma_load_3d_pair(b, &p.mapB, bar, 0, t.prow + k, t.n * 4 + crank * 2);
+        } else if (boxes == 0) {
+          ptx::tma_load_2d_pair(b, &p.mapB, bar, k, t.prow + crank * half);
+        } else {
+          for (int h = 0; h < boxes; ++h)
+            ptx::tma_load_2d_pair(b + h * 4096, &p.mapB32, bar, k, t.prow + crank * half + 32 * h);
+        }
+        ++issued;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      // CTA 0: the last copies of both CTAs have landed before the pair exits
-      if (crank == 0)
-        for (int j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
-          wait_bounded(&full[j % kStages], (j / kStages) & 1, abort_flag, p.status, p.timeout_ns, false);
+      stop = __shfl_sync(kFull, stop, 0);
     }
+    // CTA 0: the last copies of both CTAs have landed before the pair exits
+    if (crank == 0 && lane == 0)
+      for (int j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
+        wait_bounded(&full[j % kStages], (j / kStages) & 1, abort_flag, p.status, p.timeout_ns, false);
     __syncwarp();
   } else if (warp == 1) {
-    // ---- MMA issuer (CTA 0) --------------------------------------------------------------
-    if (lane == 0 && crank == 0) {
+    // ---- MMA issuer (CTA 0, lane 0; the others hold tiles) -------------------------------
+    if (crank == 0) {
+      Feed<KIND> feed;
       int stage = 0, acc = 0;
       uint32_t phase = 0;
       bool stop = false;
@@ -705,47 +734,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
                                           : ptx::sdesc_kmajor_sw128(s0 + kOpBytes);
       const uint32_t a_lo = static_cast<uint32_t>(desc_a), b_lo = static_cast<uint32_t>(desc_b);
       const uint64_t a_hi = desc_a >> 32 << 32, b_hi = desc_b >> 32 << 32;
-      for (int tile = tile0; tile < tiles && !stop; tile += tstep) {
-        const Tile t = decode<KIND>(p, scan, tile);
+      for (int tile = tile0, it = 0; tile < tiles && !stop; tile += tstep, ++it) {
+        const Tile t = feed.get(p, scan, tiles, tile0, tstep, it, lane);
         if (t.kb == 0) continue;
         const uint32_t idesc = ptx::idesc_bf16_f32(kExMTile, t.cols) | (a_mn(KIND) ? 1u << 15 : 0u) |
                                (is_dw(KIND) ? 1u << 16 : 0u);
         const int buf = acc & 1;
-        if (!wait_bounded(&tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag, p.status, p.timeout_ns, true))
-          break;
-        ptx::tc_fence_after();
         const uint32_t d = tmem + buf * 256;
-        uint32_t acc_on = 0;      // the tile's first MMA overwrites
-        for (int i = 0; i < t.kb; ++i) {
-          if (!wait_bounded(&full[stage], phase, abort_flag, p.status, p.timeout_ns, true)) {
-            stop = true;
-            break;
-          }
+        if (lane == 0) {
+          stop = !wait_bounded(&tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag, p.status, p.timeout_ns, true);
           ptx::tc_fence_after();
-          // Addresses move in the descriptors' low word only (16-byte units),
-          // so a K block costs this thread a handful of additions: built anew,
-          // eight descriptors took longer than the MMAs they feed.
-          const uint32_t at = stage * (kStageBytes >> 4);
+          uint32_t acc_on = 0;      // the tile's first MMA overwrites
+          for (int i = 0; i < t.kb && !stop; ++i) {
+            if (!wait_bounded(&full[stage], phase, abort_flag, p.status, p.timeout_ns, true)) {
+              stop = true;
+              break;
+            }
+            ptx::tc_fence_after();
+            // Addresses move in the descriptors' low word only (16-byte units),
+            // so a K block costs this thread a handful of additions: built anew,
+            // eight descriptors took longer than the MMAs they feed.
+            const uint32_t at = stage * (kStageBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < BK / UMMA_K; ++k) {
-            // K-major: along the 128-byte row; MN-major: 16 rows (two 1024-byte atoms)
-            const uint32_t da = a_lo + at + k * (a_mn(KIND) ? 2048 >> 4 : (UMMA_K * 2) >> 4);
-            const uint32_t db = b_lo + at + k * (is_dw(KIND) ? 2048 >> 4 : (UMMA_K * 2) >> 4);
-            ptx::umma_bf16_pair(d, a_hi | da, b_hi | db, idesc, acc_on);
-            acc_on = 1;
+            for (int k = 0; k < BK / UMMA_K; ++k) {
+              // K-major: along the 128-byte row; MN-major: 16 rows (two 1024-byte atoms)
+              const uint32_t da = a_lo + at + k * (a_mn(KIND) ? 2048 >> 4 : (UMMA_K * 2) >> 4);
+              const uint32_t db = b_lo + at + k * (is_dw(KIND) ? 2048 >> 4 : (UMMA_K * 2) >> 4);
+              ptx::umma_bf16_pair(d, a_hi | da, b_hi | db, idesc, acc_on);
+              acc_on = 1;
+            }
+            ptx::umma_commit_pair(&empty[stage], 0x3);
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
-          ptx::umma_commit_pair(&empty[stage], 0x3);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+          ptx::umma_commit_pair(&tfull[buf], 0x3);
         }
-        ptx::umma_commit_pair(&tfull[buf], 0x3);
         ++acc;
+        stop = __shfl_sync(kFull, stop, 0);
       }
       // no MMA may still run when TMEM is freed
-      ptx::umma_commit_pair(mma_drain, 0x1);
-      wait_bounded(mma_drain, 0, abort_flag, p.status, p.timeout_ns, false);
+      if (lane == 0) {
+        ptx::umma_commit_pair(mma_drain, 0x1);
+        wait_bounded(mma_drain, 0, abort_flag, p.status, p.timeout_ns, false);
+      }
     }
     __syncwarp();
   } else {
@@ -757,8 +790,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
     w.tid = ((warp - 2) & 3) * 32 + lane;
     w.stg = ptx::smem_u32(sEpi + w.set * set_bytes(KIND));
     int acc = 0;
+    Feed<KIND> feed;
     for (int tile = tile0, it = 0; tile < tiles; tile += tstep, ++it) {
-      const Tile t = decode<KIND>(p, scan, tile);
+      const Tile t = feed.get(p, scan, tiles, tile0, tstep, it, lane);
       w.m0 = t.m * kExMTile + crank * 128;
       const int buf = acc & 1;
       w.taddr = tmem + buf * 256 + (static_cast<uint32_t>(w.q4 * 32) << 16);
