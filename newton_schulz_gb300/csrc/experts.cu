@@ -256,8 +256,18 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 __device__ __forceinline__ float lo_of(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_of(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 __device__ __forceinline__ float f(uint32_t v) { return __uint_as_float(v); }
-// 1 / (1 + exp(-g)); results are rounded to bf16, far above these functions' errors
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// 1 / (1 + exp(-g)) by the approximate 2^x and 1 / x, each within 2 units of
+// the last place of fp32; results are rounded to bf16.
+__device__ __forceinline__ float sigmoid(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+__device__ __forceinline__ float2 sigmoid2(float2 g) { return make_float2(sigmoid(g.x), sigmoid(g.y)); }
+__device__ __forceinline__ float2 f2(uint32_t lo, uint32_t hi) { return make_float2(f(lo), f(hi)); }
+__device__ __forceinline__ float2 f2(uint32_t pair) { return make_float2(lo_of(pair), hi_of(pair)); }
+__device__ __forceinline__ uint32_t pack(float2 v) { return pack(v.x, v.y); }
 
 // 8 bf16 at p[0..8), of which the first n exist.
 __device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int n, bool vec) {
@@ -315,9 +325,33 @@ struct EpiWarp {
   __device__ void bar() const { ptx::named_bar(2 + set, 128); }
 };
 
+// Where a thread's 16-byte chunk of staged rows goes: rows `pitch` elements
+// apart from `at`, all 8 columns (full) or the first n of them.  The epilogues
+// are bound by instruction issue (two sets of four warps on an SM), so what a
+// tile fixes is worked out once a tile and the common case is a bare store.
+struct Out {
+  __nv_bfloat16* at;
+  int64_t pitch;
+  int n;
+  bool full;
+  __device__ Out(__nv_bfloat16* base, int64_t row, int64_t pitch_, int col, int limit, bool vec)
+      : at(base + row * pitch_ + col), pitch(pitch_), n(limit - col), full(vec && limit - col >= 8) {}
+  __device__ __forceinline__ void put(int row, uint32_t staged_at) const {
+    const uint4 v = lds16(staged_at);
+    if (full) *reinterpret_cast<uint4*>(at + row * pitch) = v;
+    else store8(at + row * pitch, v, n, false);
+  }
+};
+
 // gate rows and up rows sit 8 lanes apart, so one thread holds a pair
 __device__ __forceinline__ void epi_up(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
   const int f0 = w.m0 >> 1;      // first feature: half of this CTA's 128 rows are gates
+  const int orow = w.tid >> 3, chunk = w.tid & 7, ft = f0 + chunk * 8;
+  const Out act(p.act, t.prow + orow, p.ap, ft, p.ip, true);
+  const Out gate(p.gu, t.urow + orow, 2 * p.inner, ft, p.inner, p.gu_vec != 0);
+  const Out up(p.gu + p.inner, t.urow + orow, 2 * p.inner, ft, p.inner, p.gu_vec != 0);
+  const uint32_t in0 = staged(w.stg, w.lane, w.q4 * 2, 128), in1 = staged(w.stg, w.lane, w.q4 * 2 + 1, 128);
+  const uint32_t out = staged(w.stg, orow, chunk, 128);     // row + 16 keeps row % 8
   for (int c0 = w.set * 32; c0 < t.rows; c0 += 64) {
     uint32_t r[2][16];
     ptx::tmem_ld_16x256b_x4(w.taddr + c0, r[0]);
@@ -328,30 +362,27 @@ __device__ __forceinline__ void epi_up(const ExGemmParams& p, const Tile& t, con
       uint32_t a[4], g[4], u[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float g0 = f(r[b][4 * i]), g1 = f(r[b][4 * i + 1]);
-        const float u0 = f(r[b][4 * i + 2]), u1 = f(r[b][4 * i + 3]);
-        a[i] = pack(g0 * sigmoid(g0) * u0, g1 * sigmoid(g1) * u1);
-        g[i] = pack(g0, g1);
-        u[i] = pack(u0, u1);
+        const float2 gv = f2(r[b][4 * i], r[b][4 * i + 1]), uv = f2(r[b][4 * i + 2], r[b][4 * i + 3]);
+        a[i] = pack(ptx::mul2(ptx::mul2(gv, sigmoid2(gv)), uv));
+        g[i] = pack(gv);
+        u[i] = pack(uv);
       }
-      const int chunk = w.q4 * 2 + b;
-      ptx::stmatrix_x4_trans(staged(w.stg, w.lane, chunk, 128), a);
+      const uint32_t in = b ? in1 : in0;
+      ptx::stmatrix_x4_trans(in, a);
       if (p.gu) {
-        ptx::stmatrix_x4_trans(staged(w.stg + 4096, w.lane, chunk, 128), g);
-        ptx::stmatrix_x4_trans(staged(w.stg + 8192, w.lane, chunk, 128), u);
+        ptx::stmatrix_x4_trans(in + 4096, g);
+        ptx::stmatrix_x4_trans(in + 8192, u);
       }
     }
     w.bar();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int row = (w.tid >> 3) + 16 * k, chunk = w.tid & 7, ft = f0 + chunk * 8;
-      if (c0 + row >= t.rows) continue;
-      store8(p.act + static_cast<int64_t>(t.prow + c0 + row) * p.ap + ft,
-             lds16(staged(w.stg, row, chunk, 128)), p.ip - ft, true);
+      const int row = c0 + 16 * k;
+      if (row + orow >= t.rows || act.n <= 0) continue;
+      act.put(row, out + 2048 * k);
       if (p.gu) {
-        __nv_bfloat16* o = p.gu + static_cast<int64_t>(t.urow + c0 + row) * 2 * p.inner + ft;
-        store8(o, lds16(staged(w.stg + 4096, row, chunk, 128)), p.inner - ft, p.gu_vec != 0);
-        store8(o + p.inner, lds16(staged(w.stg + 8192, row, chunk, 128)), p.inner - ft, p.gu_vec != 0);
+        gate.put(row, out + 4096 + 2048 * k);
+        up.put(row, out + 8192 + 2048 * k);
       }
     }
     w.bar();
@@ -366,59 +397,68 @@ __device__ __forceinline__ void epi_up(const ExGemmParams& p, const Tile& t, con
 // 256 x [768, 2048]: 398 + 167 us with fp32 rows).  A piece that holds an
 // infinity or NaN is NaN.
 __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
-  const int piece = (w.m0 >> 5) + w.q4;
+  const int orow = w.tid >> 4, chunk = w.tid & 15, h = w.m0 + chunk * 8;
+  int16_t* const y = p.y + static_cast<int64_t>(t.urow + orow) * p.yp + h;
+  uint8_t* const ex = p.yexp + static_cast<int64_t>(t.urow + w.lane) * p.yep + (w.m0 >> 5) + w.q4;
+  const bool mine = h < p.yp;
+  const uint32_t out = staged(w.stg, orow, chunk, 256);     // row + 8 keeps row % 8
   for (int c0 = w.set * 32; c0 < t.rows; c0 += 64) {
     uint32_t r[2][16];
     ptx::tmem_ld_16x256b_x4(w.taddr + c0, r[0]);
     ptx::tmem_ld_16x256b_x4(w.taddr + (16u << 16) + c0, r[1]);
     ptx::tmem_ld_wait();
+    // rows 8 i + 2 (lane % 4) (low half) and the next (high half): upper 16 bits
+    // of the magnitudes, largest over this thread's 4 features, then the warp's 32
+    uint32_t m[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // rows 8 i + 2 (lane % 4) (low half) and the next (high half): upper
-      // 16 bits of the magnitudes, largest over this thread's 4 features, then the warp's 32
-      uint32_t m = 0;
+      m[i] = 0;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          m = __vmaxu2(m, __byte_perm(r[b][4 * i + 2 * h], r[b][4 * i + 2 * h + 1], 0x7632) & 0x7fff7fffu);
-      m = __vmaxu2(m, __shfl_xor_sync(kFull, m, 4));
-      m = __vmaxu2(m, __shfl_xor_sync(kFull, m, 8));
-      m = __vmaxu2(m, __shfl_xor_sync(kFull, m, 16));
-      const uint32_t e[2] = {(m >> 7) & 0xffu, m >> 23};
-      float s[2];
+        for (int q = 0; q < 2; ++q)
+          m[i] = __vmaxu2(m[i],
+                          __byte_perm(r[b][4 * i + 2 * q], r[b][4 * i + 2 * q + 1], 0x7632) & 0x7fff7fffu);
+    }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        s[j] = f((267u - min(max(e[j], kExpLeast), 254u)) << 23);
-        const int row = c0 + 8 * i + 2 * (w.lane & 3) + j;
-        if (w.lane < 4 && row < t.rows)
-          p.yexp[(t.urow + row) * p.yep + piece] = static_cast<uint8_t>(max(e[j], kExpLeast));
-      }
+    for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[i] = __vmaxu2(m[i], __shfl_xor_sync(kFull, m[i], o));
+    uint32_t e32 = 0;      // exponent of row c0 + lane, from a lane that holds its i and pair
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = __shfl_sync(kFull, m[i], (w.lane >> 1) & 3);
+      if ((w.lane >> 3) == i) e32 = (w.lane & 1) ? v >> 23 : (v >> 7) & 0xffu;
+    }
+    if (c0 + w.lane < t.rows) ex[c0 * p.yep] = static_cast<uint8_t>(max(e32, kExpLeast));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 s;
+      s.x = f((267u - min(max((m[i] >> 7) & 0xffu, kExpLeast), 254u)) << 23);
+      s.y = f((267u - min(max(m[i] >> 23, kExpLeast), 254u)) << 23);
       // adding 2^23 + 2^15 leaves the rounded integer plus 2^15 in the low bits
-      const float big = 8421376.f;
+      const float2 big = make_float2(8421376.f, 8421376.f);
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t* v = &r[b][4 * i + 2 * h];
-          v[0] = __byte_perm(__float_as_uint(fmaf(f(v[0]), s[0], big)),
-                             __float_as_uint(fmaf(f(v[1]), s[1], big)), 0x5410);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t* v = &r[b][4 * i + 2 * q];
+          const float2 x = ptx::fma2(f2(v[0], v[1]), s, big);
+          v[0] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x5410);
         }
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t q[4] = {r[b][2 * h], r[b][4 + 2 * h], r[b][8 + 2 * h], r[b][12 + 2 * h]};
-        ptx::stmatrix_x4_trans(staged(w.stg, w.lane, w.q4 * 4 + b * 2 + h, 256), q);
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t v[4] = {r[b][2 * q], r[b][4 + 2 * q], r[b][8 + 2 * q], r[b][12 + 2 * q]};
+        ptx::stmatrix_x4_trans(staged(w.stg, w.lane, w.q4 * 4 + b * 2 + q, 256), v);
       }
     w.bar();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int row = (w.tid >> 4) + 8 * k, chunk = w.tid & 15, h = w.m0 + chunk * 8;
-      if (c0 + row < t.rows && h < p.yp)
-        *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(t.urow + c0 + row) * p.yp + h) =
-            lds16(staged(w.stg, row, chunk, 256));
+      const int row = c0 + 8 * k;
+      if (row + orow < t.rows && mine) *reinterpret_cast<uint4*>(y + row * p.yp) = lds16(out + 2048 * k);
     }
     w.bar();
   }
@@ -436,104 +476,110 @@ __device__ __forceinline__ void fetch_weights(const ExGemmParams& p, const Tile&
 }
 
 // Gate and up rows of a slab of 32 rows, into registers: asked for a slab (and
-// a tile's first before its products are done) early, as their latency is
-// several slabs' arithmetic.
+// a tile's first before its products are done) early, as their latency is a
+// slab's arithmetic.
 struct GateUp {
   uint4 v[8];     // rows tid / 16 + 8 k of the gates, then of the ups
 };
 __device__ __forceinline__ void fetch_gu(const ExGemmParams& p, const Tile& t, const EpiWarp& w, int c0,
                                          GateUp& in) {
-  const int tok = w.tid >> 4, ft = w.m0 + (w.tid & 15) * 8;
+  const int row = c0 + (w.tid >> 4), ft = w.m0 + (w.tid & 15) * 8, n = p.inner - ft;
+  const int64_t pitch = 2 * p.inner;
+  const __nv_bfloat16* q = p.gu + (t.urow + row) * pitch + ft;
+  if (p.gu_vec && n >= 8) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int row = c0 + tok + 8 * (k & 3);
-    const __nv_bfloat16* q =
-        p.gu + static_cast<int64_t>(t.urow + row) * 2 * p.inner + (k >> 2) * p.inner + ft;
-    in.v[k] = load8(q, row < t.valid ? p.inner - ft : 0, p.gu_vec != 0);
+    for (int k = 0; k < 4; ++k) {
+      in.v[k] = in.v[k + 4] = make_uint4(0u, 0u, 0u, 0u);
+      if (row + 8 * k < t.valid) {
+        in.v[k] = *reinterpret_cast<const uint4*>(q + 8 * k * pitch);
+        in.v[k + 4] = *reinterpret_cast<const uint4*>(q + 8 * k * pitch + p.inner);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      in.v[k] = load8(q + 8 * (k & 3) * pitch + (k >> 2) * p.inner, row + 8 * (k & 3) < t.valid ? n : 0, false);
   }
 }
 
 // da -> dgu, w a and this warp's 32 features' part of <da, a>; 32 rows at a time
 __device__ __forceinline__ void epi_dact(const ExGemmParams& p, const Tile& t, const EpiWarp& w, GateUp& in) {
-  const int tok = w.tid >> 4, chunk = w.tid & 15, ft = w.m0 + chunk * 8;
+  const int orow = w.tid >> 4, chunk = w.tid & 15, ft = w.m0 + chunk * 8;
   constexpr uint32_t kUp = 8192, kAct = 16384;
+  const Out dg_out(p.dgu, t.prow + orow, p.gp, ft, p.ip, true);
+  const Out du_out(p.dgu + p.ip, t.prow + orow, p.gp, ft, p.ip, true);
+  const Out wa_out(p.act, t.prow + orow, p.ap, ft, p.ip, true);
+  const uint32_t own = staged(w.stg, orow, chunk, 256);     // row + 8 keeps row % 8
+  float* const part = p.part + ((w.m0 >> 5) + w.q4) * p.rows + t.urow + 2 * (w.lane & 3);
+  const bool parts = w.lane < 4 && w.m0 < p.m;
+  // ldmatrix / stmatrix: matrix 2 i + c is rows 8 i.. of 8 features, chunk c of a 16-lane block
+  const int lr = (w.lane >> 4) * 8 + (w.lane & 7), lc = w.q4 * 4 + ((w.lane >> 3) & 1);
+  const uint32_t mat[2] = {staged(w.stg, lr, lc, 256), staged(w.stg, lr, lc + 2, 256)};
   for (int c0 = w.set * 32; c0 < t.rows; c0 += 64) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      sts16(staged(w.stg + (k >> 2) * kUp, tok + 8 * (k & 3), chunk, 256), in.v[k]);
+    for (int k = 0; k < 8; ++k) sts16(own + (k >> 2) * kUp + (k & 3) * 2048, in.v[k]);
     if (c0 + 64 < t.rows) fetch_gu(p, t, w, c0 + 64, in);
     w.bar();
 #pragma unroll
     for (int s = 0; s < 2; ++s) {       // 16 rows
       const int cs = c0 + 16 * s;
-      float wt[2][2], dot[2][2];
+      float2 wt[2], dot[2];             // rows cs + 8 i + 2 (lane % 4) and the next
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int row = cs + 8 * i + 2 * (w.lane & 3) + j;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(wt[i][j]) : "r"(w.stg + kWeightOff + row * 4) : "memory");
-          dot[i][j] = 0.f;
-        }
+      for (int i = 0; i < 2; ++i) {
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(wt[i].x), "=f"(wt[i].y)
+                     : "r"(w.stg + kWeightOff + (cs + 8 * i + 2 * (w.lane & 3)) * 4)
+                     : "memory");
+        dot[i] = make_float2(0.f, 0.f);
+      }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        uint32_t r[8];
+        uint32_t r[8], g[4], u[4], a[4];
         ptx::tmem_ld_16x256b_x2(w.taddr + (static_cast<uint32_t>(b * 16) << 16) + cs, r);
-        // matrix 2 i + c: rows 8 i.. of 8 features, chunk c of this 16-lane block
-        const int lr = 16 * s + (w.lane >> 4) * 8 + (w.lane & 7);
-        const int lc = w.q4 * 4 + b * 2 + ((w.lane >> 3) & 1);
-        uint32_t g[4], u[4], a[4];
-        ptx::ldmatrix_x4_trans(staged(w.stg, lr, lc, 256), g);
-        ptx::ldmatrix_x4_trans(staged(w.stg + kUp, lr, lc, 256), u);
+        const uint32_t at = mat[b] + s * 4096;
+        ptx::ldmatrix_x4_trans(at, g);
+        ptx::ldmatrix_x4_trans(at + kUp, u);
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const uint32_t gv = g[2 * i + c], uv = u[2 * i + c];
-            float dg[2], du[2], wa[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float gg = j ? hi_of(gv) : lo_of(gv), uu = j ? hi_of(uv) : lo_of(uv);
-              const float da = f(r[4 * i + 2 * c + j]);
-              const float sg = sigmoid(gg), sl = gg * sg;
-              dot[i][j] = fmaf(da, sl * uu, dot[i][j]);
-              const float wd = wt[i][j] * da;
-              dg[j] = wd * uu * (sg * (1.f + gg * (1.f - sg)));
-              du[j] = wd * sl;
-              wa[j] = wt[i][j] * (sl * uu);
-            }
-            g[2 * i + c] = pack(dg[0], dg[1]);
-            u[2 * i + c] = pack(du[0], du[1]);
-            a[2 * i + c] = pack(wa[0], wa[1]);
+            const float2 gv = f2(g[2 * i + c]), uv = f2(u[2 * i + c]);
+            const float2 da = f2(r[4 * i + 2 * c], r[4 * i + 2 * c + 1]);
+            const float2 sg = sigmoid2(gv);
+            const float2 sl = ptx::mul2(gv, sg), act = ptx::mul2(sl, uv), wd = ptx::mul2(wt[i], da);
+            dot[i] = ptx::fma2(da, act, dot[i]);
+            // silu' = s (1 + g - g s) = s + sl - sl s
+            const float2 slope = ptx::fma2(make_float2(-sl.x, -sl.y), sg, ptx::add2(sl, sg));
+            g[2 * i + c] = pack(ptx::mul2(ptx::mul2(wd, uv), slope));
+            u[2 * i + c] = pack(ptx::mul2(wd, sl));
+            a[2 * i + c] = pack(ptx::mul2(wt[i], act));
           }
         // a warp reads and writes its own four chunks only
-        ptx::stmatrix_x4_trans(staged(w.stg, lr, lc, 256), g);
-        ptx::stmatrix_x4_trans(staged(w.stg + kUp, lr, lc, 256), u);
-        ptx::stmatrix_x4_trans(staged(w.stg + kAct, lr, lc, 256), a);
+        ptx::stmatrix_x4_trans(at, g);
+        ptx::stmatrix_x4_trans(at + kUp, u);
+        ptx::stmatrix_x4_trans(at + kAct, a);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float v = dot[i][j];
-          v += __shfl_xor_sync(kFull, v, 4);
-          v += __shfl_xor_sync(kFull, v, 8);
-          v += __shfl_xor_sync(kFull, v, 16);
-          const int row = cs + 8 * i + 2 * (w.lane & 3) + j;
-          if (w.lane < 4 && row < t.valid && w.m0 < p.m)
-            p.part[((w.m0 >> 5) + w.q4) * p.rows + t.urow + row] = v;
+        for (int o = 4; o < 32; o <<= 1) {
+          dot[i].x += __shfl_xor_sync(kFull, dot[i].x, o);
+          dot[i].y += __shfl_xor_sync(kFull, dot[i].y, o);
         }
+        const int row = cs + 8 * i + 2 * (w.lane & 3);
+        if (parts && row < t.valid) part[cs + 8 * i] = dot[i].x;
+        if (parts && row + 1 < t.valid) part[cs + 8 * i + 1] = dot[i].y;
+      }
     }
     w.bar();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int row = tok + 8 * k;
-      if (c0 + row >= t.rows) continue;
-      const int64_t at = t.prow + c0 + row;
-      store8(p.dgu + at * p.gp + ft, lds16(staged(w.stg, row, chunk, 256)), p.ip - ft, true);
-      store8(p.dgu + at * p.gp + p.ip + ft, lds16(staged(w.stg + kUp, row, chunk, 256)), p.ip - ft, true);
-      store8(p.act + at * p.ap + ft, lds16(staged(w.stg + kAct, row, chunk, 256)), p.ip - ft, true);
+      const int row = c0 + 8 * k;
+      if (row + orow >= t.rows || dg_out.n <= 0) continue;
+      dg_out.put(row, own + k * 2048);
+      du_out.put(row, own + kUp + k * 2048);
+      wa_out.put(row, own + kAct + k * 2048);
     }
     w.bar();
   }
