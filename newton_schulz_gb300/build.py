@@ -28,7 +28,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cpp", "ns_plan.cpp", "elementwise.cu", "ns_gemm.cu", "ns_small.cu", "noalloc.cu", "adamw.cu", "owners.cpp",
            "block_api.cpp", "rmsnorm.cu", "route.cu", "experts.cu", "experts_few.cu"]
-HEADERS = ["muon_internal.h", "block.h", "sm100_ptx.cuh"]
+HEADERS = ["muon_internal.h", "block.h", "sm100_ptx.cuh", "block_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]

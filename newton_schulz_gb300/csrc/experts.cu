@@ -46,7 +46,7 @@
 #include <algorithm>
 
 #include "block.h"
-#include "sm100_ptx.cuh"
+#include "block_ptx.cuh"
 
 namespace muon {
 

@@ -6,7 +6,7 @@
 // took 34 us on 48 and 64 of their 76 CTA pairs' tiles, without the copy and
 // the sum over slots that they need besides.
 #include "block.h"
-#include "sm100_ptx.cuh"
+#include "block_ptx.cuh"
 
 namespace muon {
 

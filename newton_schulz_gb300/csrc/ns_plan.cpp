@@ -53,24 +53,6 @@ bool encode_tiled(CUtensorMap* map, bool f32, const void* base, const uint64_t* 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_bf16_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                    const uint64_t* strides, const uint32_t* box) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn || rank < 2 || rank > 5) return false;
-  cuuint64_t d[5], st[4];
-  cuuint32_t b[5], estr[5];
-  for (int i = 0; i < rank; ++i) {
-    d[i] = dims[i];
-    b[i] = box[i];
-    estr[i] = 1;
-    if (i + 1 < rank) st[i] = strides[i];
-  }
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
-            const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool make_ns_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t cnt,
                  int64_t pitch, int64_t mstride, int box_rows) {
   const uint64_t dims[3] = {static_cast<uint64_t>(inner), static_cast<uint64_t>(rows),

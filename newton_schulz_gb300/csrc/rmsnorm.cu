@@ -15,7 +15,7 @@
 #include <type_traits>
 
 #include "block.h"
-#include "sm100_ptx.cuh"
+#include "block_ptx.cuh"
 
 namespace muon {
 
