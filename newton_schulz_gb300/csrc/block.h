@@ -67,7 +67,7 @@ struct NormParams {
   int grouped;                        // e4m3: a scale per 128 columns (0: per row)
   int n_scales;                       // scales per row
   int vec;                            // 16-byte accesses are legal
-  float eps;
+  float eps, inv_cols;                // inv_cols = 1 / cols
 };
 
 struct NormGradParams {
@@ -81,7 +81,7 @@ struct NormGradParams {
   int cols;
   int dy_dt, h_dt, g_dt, dr_dt, dh_dt;
   int vec;
-  float eps;
+  float eps, inv_cols;
   unsigned* status;
   unsigned long long timeout_ns;
 };

@@ -97,7 +97,7 @@ muon_status_t norm_impl(const muon_rmsnorm_t* a, cudaStream_t stream) {
   p.y_dt = a->y_dtype;
   p.grouped = a->group != 0;
   p.n_scales = static_cast<int>(n_scales);
-  p.eps = a->eps;
+  p.eps = a->eps, p.inv_cols = 1.f / static_cast<float>(a->cols);
   p.vec = x.rows16() && r.rows16() && h.rows16() && y.rows16() && g.rows16();
   std::lock_guard<std::mutex> lock(api_mutex());
   ApiDevice d;
@@ -146,7 +146,7 @@ muon_status_t norm_grad_impl(const muon_rmsnorm_grad_t* a, cudaStream_t stream) 
   p.dy_dt = a->dy_dtype, p.h_dt = a->h_dtype, p.dh_dt = a->dh_dtype;
   p.g_dt = a->gain ? a->gain_dtype : kDtNone;
   p.dr_dt = a->dres ? a->dres_dtype : kDtNone;
-  p.eps = a->eps;
+  p.eps = a->eps, p.inv_cols = 1.f / static_cast<float>(a->cols);
   p.vec = dy.rows16() && h.rows16() && dr.rows16() && dh.rows16() && g.rows16();
   std::lock_guard<std::mutex> lock(api_mutex());
   ApiDevice d;

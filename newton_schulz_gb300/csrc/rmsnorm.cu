@@ -8,7 +8,10 @@
 // HBM-bound: every input is read once and every output written once; a row
 // stays in registers between its statistics and its outputs.  A row is taken
 // by `tpr` threads of 8-column chunks (chunk i * tpr + t): part of a warp, or
-// a whole block.  All arithmetic is fp32; each output is rounded once.
+// a whole block.  All arithmetic is fp32; each output is rounded once.  The
+// reciprocal root and the codes' factor are CUDA's approximate ones (within 2
+// units of the last place): with 256 threads a row, exact divisions by each of
+// them were a fifth of the instructions.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -236,7 +239,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const Chunk<WIDE> 
     }
   }
   const float ss = row_reduce<false>(s2.x + s2.y, tpr, s_sum);
-  const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.cols) + p.eps);
+  const float rstd = rsqrtf(fmaf(ss, p.inv_cols, p.eps));
   const float2 r2 = make_float2(rstd, rstd);
   // gain * h * rstd of chunk i
   auto scaled = [&](int i, float (&o)[8]) {
@@ -273,17 +276,17 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const Chunk<WIDE> 
     for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = fmaxf(m, 1e-12f);
     if (live && col < p.cols) {
-      const float k = 448.f / m;
+      const float k = __fdividef(448.f, m);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= k;
       store_chunk(yr, kDtE4m3, col, p.cols, vec, v);
-      if ((c & 15) == 0) p.scales[row * p.n_scales + (c >> 4)] = m / 448.f;
+      if ((c & 15) == 0) p.scales[row * p.n_scales + (c >> 4)] = m * (1.f / 448.f);
     }
   }
   if (!e4m3 || p.grouped) return;
   // one scale for the row
   top = fmaxf(row_reduce<true>(top, tpr, s_max), 1e-12f);
-  const float k = 448.f / top;
+  const float k = __fdividef(448.f, top);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int col = (i * tpr + t) * 8;
@@ -293,7 +296,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const Chunk<WIDE> 
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= k;
     store_chunk(yr, kDtE4m3, col, p.cols, vec, v);
-    if (col == 0) p.scales[row] = top / 448.f;
+    if (col == 0) p.scales[row] = top * (1.f / 448.f);
   }
 }
 
@@ -402,9 +405,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 8 ? 512 : 256, NV == 2 
       }
     }
     row_reduce2(ss, dot, tpr, s_a[par], s_b[par]);
-    const float n = static_cast<float>(p.cols);
-    const float rstd = 1.f / sqrtf(ss / n + p.eps);
-    const float m = dot * rstd / n;      // mean(gain dy u)
+    const float rstd = rsqrtf(fmaf(ss, p.inv_cols, p.eps));
+    const float m = dot * rstd * p.inv_cols;      // mean(gain dy u)
     char* out = row_ptr(p.dh, p.dh_dt, row, p.dhs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -479,7 +481,6 @@ __global__ void __launch_bounds__(256, 2)
       acc[i][j] = make_float2(0.f, 0.f);
     }
   }
-  const float n = static_cast<float>(p.cols);
   int s = 0, par = 0;
   uint32_t phase = 0;
   for (int64_t row = blockIdx.x; row < rows; row += step) {
@@ -512,8 +513,8 @@ __global__ void __launch_bounds__(256, 2)
       s = 0;
       phase ^= 1;
     }
-    const float rstd = 1.f / sqrtf(ss / n + p.eps);
-    const float m = -rstd * rstd * (dot * rstd / n);
+    const float rstd = rsqrtf(fmaf(ss, p.inv_cols, p.eps));
+    const float m = -rstd * rstd * (dot * rstd * p.inv_cols);
     const float2 r2 = make_float2(rstd, rstd), m2 = make_float2(m, m);
     char* out = row_ptr(p.dh, p.dh_dt, row, p.dhs);
 #pragma unroll
@@ -592,9 +593,7 @@ cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t s) {
   // flight a thread.
   const int chunks = (p.cols + 7) / 8;
   const bool wide = p.x_dt != kDtBf16 || (p.r_dt != kDtNone && p.r_dt != kDtBf16);
-  const int nv = p.rows <= 4 * sms && chunks <= 1024 ? 1
-                 : wide && p.rows <= 64 * sms && chunks <= 256 ? 1
-                 : wide && chunks <= 512 ? 2 : chunks <= 1024 ? 4 : 8;
+  const int nv = p.rows <= 4 * sms && chunks <= 1024 ? 1 : wide && chunks <= 512 ? 2 : chunks <= 1024 ? 4 : 8;
   const int tpr = threads_per_row(p.cols, nv, 16);
   const int block = tpr > 32 ? tpr : 128;
   const int64_t grid = (p.rows + block / tpr - 1) / (block / tpr);

@@ -178,20 +178,28 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
         }
       }
     }
-    // this lane's largest key, the lowest expert among equal ones
-    uint32_t a;
-    int at;
+    // this lane's two largest keys, lower experts first among equal ones: a lane
+    // is looked through again only when it gives its third expert
+    uint32_t a = 0u, a2 = 0u, used = 0u;
+    int at = 0, at2 = 0;
     auto rescan = [&] {
-      a = key[0];
-      at = 0;
+      a = a2 = 0u;
 #pragma unroll
-      for (int i = 1; i < EPL; ++i)
-        if (key[i] > a) {
-          a = key[i];
+      for (int i = 0; i < EPL; ++i) {
+        const uint32_t v = (used >> i) & 1u ? 0u : key[i];
+        if (v > a) {
+          a2 = a;
+          at2 = at;
+          a = v;
           at = i;
+        } else if (v > a2) {
+          a2 = v;
+          at2 = i;
         }
+      }
     };
     rescan();
+    bool second = true;      // a2 is the next after a
     for (int j = 0; j < k; ++j) {
       const uint32_t m = __reduce_max_sync(kFull, a);
       if (!m) break;
@@ -204,10 +212,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
       }
       if (lane == j) my_idx = e;
       if (lane == owner) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (i == at) key[i] = 0u;
-        rescan();
+        used |= 1u << at;
+        if (second) {
+          a = a2;
+          at = at2;
+          second = false;
+        } else {
+          rescan();
+          second = true;
+        }
       }
     }
     // the chosen experts' scores, each in its lane, from the logit again (in L1)
@@ -252,20 +265,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     e = p.idx[tok * p.top_k + lane];
     dw = p.dweights[tok * p.top_k + lane] * p.scale;
   }
-  uint32_t chosen = 0;    // bit i: expert i * 32 + lane is chosen
+  // each chosen expert's dweight to its lane and register, through shared memory
+  __shared__ float s_d[kRouteWarps][EPL * 32];
+  __shared__ uint32_t s_chosen[kRouteWarps][32];
+  const int warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) d[i] = 0.f;
-  for (int j = 0; j < p.top_k; ++j) {
-    const int32_t ej = __shfl_sync(kFull, e, j);
-    const float dj = __shfl_sync(kFull, dw, j);
-    if (ej < 0 || ej >= p.experts || (ej & 31) != lane) continue;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (i == (ej >> 5)) {
-        d[i] = dj;
-        chosen |= 1u << i;
-      }
+  for (int i = 0; i < EPL; ++i) s_d[warp][i * 32 + lane] = 0.f;
+  s_chosen[warp][lane] = 0u;
+  __syncwarp();
+  if (e >= 0 && e < p.experts) {
+    s_d[warp][e] = dw;
+    atomicOr(&s_chosen[warp][e & 31], 1u << (e >> 5));
   }
+  __syncwarp();
+  const uint32_t chosen = s_chosen[warp][lane];    // bit i: expert i * 32 + lane is chosen
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) d[i] = s_d[warp][i * 32 + lane];
   if (p.renorm) {
     float total = 0.f, dot = 0.f;
 #pragma unroll
@@ -349,9 +364,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   // this tile's counts per warp
   const int64_t run = (end - first + kPlanWarps * 32 - 1) / (kPlanWarps * 32) * 32;
   const int64_t w0 = first + warp * run, w1 = min(w0 + run, end);
-  for (int64_t i = w0 + lane; i < w1; i += 32) {
-    const int e = expert_of(p, i, w1);
-    if (e >= 0) atomicAdd(&start[warp * E + e], 1);
+  for (int64_t i0 = w0 + lane; i0 < w1; i0 += 128) {      // four loads in flight
+    int e[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e[j] = expert_of(p, i0 + 32 * j, w1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (e[j] >= 0) atomicAdd(&start[warp * E + e[j]], 1);
   }
   __syncthreads();
   // expert totals and the entries of earlier tiles; exclusive scan over experts
