@@ -486,6 +486,15 @@ def _rows(t, name: str, cols: Optional[int] = None, rows: Optional[int] = None):
     return t.data_ptr(), stride, _code(t.dtype)
 
 
+def _like(t, dtype=None):
+    """An uninitialised contiguous tensor of t's shape (torch.empty_like is the
+    cheapest allocation from Python; it would keep a view's strides)."""
+    import torch
+    if t.is_contiguous():
+        return torch.empty_like(t) if dtype is None else torch.empty_like(t, dtype=dtype)
+    return torch.empty(t.shape, dtype=dtype or t.dtype, device=t.device)
+
+
 def _dense(t, name: str, shape, dtype) -> int:
     """Pointer of a contiguous CUDA tensor of exactly this shape and dtype."""
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
@@ -510,20 +519,20 @@ def muon_rmsnorm_forward(x, gain=None, residual=None, eps: float = 1e-6, y_dtype
     if residual is not None:
         rp, rs, rc = _rows(residual, "residual", cols, rows)
         if h is None:
-            h = residual.new_empty((rows, cols))
+            h = _like(residual)
     if gain is not None:
         gp, gc = _dense(gain, "gain", (cols,), gain.dtype), _code(gain.dtype)
     if h is not None:
         hp, hs, hc = _rows(h, "h", cols, rows)
     if y is None:
-        y = x.new_empty((rows, cols), dtype=y_dtype)
+        y = _like(x, y_dtype)
     elif y_dtype is not None and y.dtype != y_dtype:
         raise ValueError(f"y is {y.dtype}, expected {y_dtype}")
     yp, ys, yc = _rows(y, "y", cols, rows)
     if yc == MUON_E4M3:
         n = -(-cols // group) if group > 0 else 1
         if scales is None:
-            scales = x.new_empty((rows, n), dtype=torch.float32)
+            scales = torch.empty((rows, n), dtype=torch.float32, device=x.device)
         sp = _dense(scales, "scales", (rows, n), torch.float32)
     else:
         scales = None
@@ -548,10 +557,10 @@ def muon_rmsnorm_backward(dy, h, gain=None, dres=None, eps: float = 1e-6, dh=Non
     if dres is not None:
         rp, rs, rc = _rows(dres, "dres", cols, rows)
     if dh is None:
-        dh = h.new_empty((rows, cols))
+        dh = _like(h)
     op, os_, oc = _rows(dh, "dh", cols, rows)
     if dgain is None and want_dgain:
-        dgain = dy.new_empty(cols, dtype=torch.float32)
+        dgain = torch.empty(cols, dtype=torch.float32, device=dy.device)
     if dgain is not None:
         wp = _dense(dgain, "dgain", (cols,), torch.float32)
     a = RmsNormGrad(rows, cols, dp, ds, hp, hs, gp, rp, rs, op, os_, wp, dc, hc, gc, rc, oc, eps)
@@ -567,11 +576,11 @@ def make_route_config(experts: int, top_k: int, score: int = ROUTE_SOFTMAX, grou
                        group_score, int(renormalize), scale)
 
 
-def _plan_tensors(like, tokens: int, top_k: int, experts: int):
+def _plan_tensors(dev, tokens: int, top_k: int, experts: int):
     import torch
-    return (like.new_empty(experts + 1, dtype=torch.int32),
-            like.new_empty(tokens * top_k, dtype=torch.int32),
-            like.new_empty((tokens, top_k), dtype=torch.int32))
+    return (torch.empty(experts + 1, dtype=torch.int32, device=dev),
+            torch.empty(tokens * top_k, dtype=torch.int32, device=dev),
+            torch.empty((tokens, top_k), dtype=torch.int32, device=dev))
 
 
 def muon_route_forward(logits, cfg: RouteConfig, bias=None, mask=None, plan: bool = True,
@@ -582,12 +591,12 @@ def muon_route_forward(logits, cfg: RouteConfig, bias=None, mask=None, plan: boo
     [tokens], tokens to leave out are false."""
     import torch
     ptr, stride, code = _rows(logits, "logits", cfg.experts)
-    tokens, k = logits.shape[0], cfg.top_k
-    idx = logits.new_empty((tokens, k), dtype=torch.int32)
-    weights = logits.new_empty((tokens, k), dtype=torch.float32)
+    tokens, k, dev = logits.shape[0], cfg.top_k, logits.device
+    idx = torch.empty((tokens, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
     off = src = pos = op = sp = pp = None
     if plan:
-        off, src, pos = _plan_tensors(logits, tokens, k, cfg.experts)
+        off, src, pos = _plan_tensors(dev, tokens, k, cfg.experts)
         op, sp, pp = off.data_ptr(), src.data_ptr(), pos.data_ptr()
     b = _dense(bias, "bias", (cfg.experts,), torch.float32) if bias is not None else None
     m = None
@@ -604,7 +613,7 @@ def muon_route_plan(idx, experts: int, stream=None):
     import torch
     tokens, top_k = idx.shape
     p = _dense(idx, "idx", (tokens, top_k), torch.int32)
-    off, src, pos = _plan_tensors(idx, tokens, top_k, experts)
+    off, src, pos = _plan_tensors(idx.device, tokens, top_k, experts)
     check(load().muon_route_plan(p, tokens, top_k, experts, off.data_ptr(), src.data_ptr(),
                                  pos.data_ptr(), _stream_ptr(stream)), "muon_route_plan")
     return off, src, pos
@@ -616,7 +625,7 @@ def muon_route_backward(logits, cfg: RouteConfig, idx, dweights, dlogits=None, s
     ptr, stride, code = _rows(logits, "logits", cfg.experts)
     tokens = logits.shape[0]
     if dlogits is None:
-        dlogits = logits.new_empty((tokens, cfg.experts))
+        dlogits = _like(logits)
     dptr, dstride, dcode = _rows(dlogits, "dlogits", cfg.experts, tokens)
     if dcode != code:
         raise ValueError("dlogits must have the logits' dtype")
@@ -657,13 +666,13 @@ def muon_experts_forward(x, w_in, w_out, route: Route, save: bool = False, out=N
     import torch
     a = _experts_args(x, w_in, w_out, route)
     if out is None:
-        out = x.new_empty((a.tokens, a.hidden))
+        out = _like(x)
     elif out.dtype != torch.bfloat16:
         raise TypeError(f"out must be bfloat16, got {out.dtype}")
     optr, ostride, _ = _rows(out, "out", a.hidden, a.tokens)
     gu = None
     if save:
-        gu = x.new_empty((a.tokens * a.top_k, 2 * a.inner))
+        gu = torch.empty((a.tokens * a.top_k, 2 * a.inner), dtype=torch.bfloat16, device=x.device)
     check(load().muon_experts_forward(a, optr, ostride,
                                       gu.data_ptr() if save else None, _stream_ptr(stream)),
           "muon_experts_forward")
@@ -685,17 +694,17 @@ def muon_experts_backward(dout, x, w_in, w_out, route: Route, gu, dw_dtype=None,
     g = _dense(gu, "gu", (a.tokens * a.top_k, 2 * a.inner), bf16)
     xptr, xstride = None, a.hidden
     if dx is None and want_dx:
-        dx = x.new_empty((a.tokens, a.hidden))
+        dx = _like(x)
     if dx is not None:
         xptr, xstride, _ = _rows(dx, "dx", a.hidden, a.tokens)
     if want_dw:
         dw_dtype = dw_dtype or (dw_in.dtype if dw_in is not None else torch.float32)
         if dw_in is None:
-            dw_in = w_in.new_empty(w_in.shape, dtype=dw_dtype)
+            dw_in = torch.empty_like(w_in, dtype=dw_dtype)
         if dw_out is None:
-            dw_out = w_out.new_empty(w_out.shape, dtype=dw_dtype)
+            dw_out = torch.empty_like(w_out, dtype=dw_dtype)
     code = _code(dw_dtype) if dw_dtype is not None else MUON_F32
-    dweights = x.new_empty((a.tokens, a.top_k), dtype=torch.float32)
+    dweights = torch.empty((a.tokens, a.top_k), dtype=torch.float32, device=x.device)
     check(load().muon_experts_backward(
         a, dptr, dstride, g, xptr, xstride,
         _dense(dw_in, "dw_in", w_in.shape, dw_dtype) if want_dw else None,
