@@ -230,21 +230,21 @@ struct Feed {
   }
 };
 
+// Waits are suspended in the hardware (up to 100 us at a time), not polled.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                              unsigned* status, unsigned long long timeout_ns,
                                              bool honour_abort) {
+  constexpr uint32_t kSuspendNs = 100000;
   const uint32_t addr = ptx::smem_u32(bar);
-  if (ptx::mbar_try_wait(addr, parity)) return true;
+  if (ptx::mbar_try_wait_for(addr, parity, kSuspendNs)) return true;
   const uint64_t t0 = ptx::globaltimer();
-  for (uint32_t it = 1;; ++it) {
-    if (ptx::mbar_try_wait(addr, parity)) return true;
-    if ((it & 255u) == 0) {
-      if (honour_abort && *abort_flag) return false;
-      if (ptx::globaltimer() - t0 > timeout_ns) {
-        atomicOr(status, kDevTimeout);
-        *abort_flag = 1;
-        return false;
-      }
+  for (;;) {
+    if (ptx::mbar_try_wait_for(addr, parity, kSuspendNs)) return true;
+    if (honour_abort && *abort_flag) return false;
+    if (ptx::globaltimer() - t0 > timeout_ns) {
+      atomicOr(status, kDevTimeout);
+      *abort_flag = 1;
+      return false;
     }
   }
 }
@@ -848,10 +848,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
         if (w.set * 32 < t.rows) fetch_gu(p, t, w, w.set * 32, in);
       }
       if (t.kb > 0) {
-        wait_bounded(&tfull[buf], (acc >> 1) & 1, abort_flag, p.status, p.timeout_ns, false);
-        // one decision for the set (its warps share a barrier); the slot
-        // alternates, so it is rewritten only after everyone has read it
-        if (w.tid == 0) s_ok[2 * w.set + (it & 1)] = !*abort_flag;
+        // One thread of the set waits and decides for all (they share a barrier,
+        // which costs nothing while it holds them); the slot alternates, so it is
+        // rewritten only after everyone has read it.
+        if (w.tid == 0) {
+          wait_bounded(&tfull[buf], (acc >> 1) & 1, abort_flag, p.status, p.timeout_ns, false);
+          s_ok[2 * w.set + (it & 1)] = !*abort_flag;
+        }
         w.bar();
         if (!s_ok[2 * w.set + (it & 1)]) break;
         ptx::tc_fence_after();
