@@ -161,6 +161,7 @@ struct ExGemmParams {
   int pad;                        // padded row numbering: segments of 1 or kExSeg rows
   int m_tiles, n_tiles;           // M tiles of a pair; kExDw*: N tiles
   int kb;                         // K blocks of 64 (kExDw*: from the expert's rows)
+  int pairs;                      // CTA pairs per cluster, 1 or 2
   int m, n;                       // valid M (padded for kExDwIn) and, kExDw*, N
   int inner, ip;                  // inner, and rounded up to 8
   int ap, gp;                     // pitches of act and dgu

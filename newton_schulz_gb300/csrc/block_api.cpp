@@ -446,21 +446,22 @@ bool map2(CUtensorMap* m, const void* base, int64_t d0, int64_t d1, int64_t pitc
 }
 // Token rows, in boxes of 128 and of 32.
 bool map_rows(ExGemmParams* p, const void* base, int64_t d0, int64_t rows, int64_t pitch) {
-  return map2(&p->mapB, base, d0, rows, pitch, 128) && map2(&p->mapB32, base, d0, rows, pitch, 32);
+  return map2(&p->mapB, base, d0, rows, pitch, 128 / p->pairs) && map2(&p->mapB32, base, d0, rows, pitch, 32);
 }
-// A matrix read MN-major in one copy: columns as chunks of 64, box 64 x 64 x 2.
+// A matrix read MN-major in one copy: columns as chunks of 64, box 64 x 64 x chunks.
 // `cols` is a multiple of 64; rows of d2 matrices.
-bool map_mn(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t pitch, int64_t d2) {
+bool map_mn(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t pitch, int64_t d2,
+            uint32_t chunks) {
   const uint64_t dims[4] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols / 64),
                             static_cast<uint64_t>(d2)};
   const uint64_t st[3] = {static_cast<uint64_t>(pitch * 2), 128, static_cast<uint64_t>(pitch * rows * 2)};
-  const uint32_t box[4] = {64, 64, 2, 1};
+  const uint32_t box[4] = {64, 64, chunks, 1};
   return encode_bf16_nd(m, base, d2 ? 4 : 3, dims, st, box);
 }
 // MN-major weights [e][rows][cols]: in one copy where the columns are whole chunks.
 bool map_weights_mn(ExGemmParams* p, const void* base, int64_t cols, int64_t rows, int64_t pitch) {
   p->a_whole = cols % 64 == 0;
-  return p->a_whole ? map_mn(&p->mapA, base, cols, rows, pitch, p->experts)
+  return p->a_whole ? map_mn(&p->mapA, base, cols, rows, pitch, p->experts, 2)
                     : map3(&p->mapA, base, cols, rows, p->experts, pitch, 64);
 }
 // W_in as [e][ip / 8][gate, up][8][hidden]: a box of 64 x 8 x 2 x 8 is 128
@@ -474,7 +475,23 @@ bool map_up(CUtensorMap* m, const void* base, const muon_experts_t* a, const Wei
   return encode_bf16_nd(m, base, 5, dims, st, box);
 }
 
-ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const ApiDevice& d, int pad) {
+int tiles_of(int64_t n, int64_t per) { return static_cast<int>((n + per - 1) / per); }
+
+// Two CTA pairs to a cluster, one M tile each over the same column tile, whose
+// halves each pair loads for both: a quarter less is read from the second-level
+// cache, which a power-capped GPU turns into clock (2.9 TFLOP over 8 experts:
+// 1972 -> 1864 us).  It needs products that the tensor cores bound: 256 rows an
+// expert and 16 steps of K (768 columns, 12 steps: 1172 -> 1176), and M tiles
+// that pair up but for one in nine.  Such clusters fit on 144 of 152 SMs, so
+// what waits for memory is better off without (48 tokens over 256 experts:
+// 233 -> 244).
+int pairs_for(const muon_experts_t* a, int64_t rows, int64_t m_rows, int64_t k) {
+  const int64_t m_tiles = tiles_of(m_rows, kExMTile);
+  return rows >= int64_t{256} * a->experts && k >= 1024 && (m_tiles % 2 == 0 || m_tiles >= 9) ? 2 : 1;
+}
+
+ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const ApiDevice& d, int pad, int64_t m_rows,
+                         int pairs) {
   ExGemmParams p;
   std::memset(&p, 0, sizeof(p));
   p.offsets = a->offsets;
@@ -482,6 +499,8 @@ ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const Api
   p.experts = a->experts;
   p.e0 = 0, p.e1 = a->experts;
   p.pad = pad;
+  p.pairs = pairs;
+  p.m_tiles = tiles_of(m_rows, kExMTile * pairs);
   p.inner = static_cast<int>(a->inner), p.ip = static_cast<int>(w.ip);
   p.ap = p.ip, p.gp = 2 * p.ip;
   p.status = d.status, p.timeout_ns = d.timeout_ns;
@@ -527,8 +546,6 @@ struct RowPlan {
 
 constexpr int kGatherBlocks = 5;      // per SM, for a copy that runs alone
 constexpr int64_t kBesideRows = 16384;      // from here a copy takes longer than its overlap costs
-
-int tiles_of(int64_t n, int64_t per) { return static_cast<int>((n + per - 1) / per); }
 
 // Many rows: the copy of the first experts' rows runs alone, that of the rest
 // while the first experts' product runs (the copy needs HBM, the product the
@@ -598,13 +615,13 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
     g.e0 = part, g.e1 = a->experts;
   }
   MUON_TRY(c.run(launch_ex_gather(g, rows, (part ? 1 : kGatherBlocks) * d.sms, stream)));
-  ExGemmParams up = gemm_params(a, w, d, 1);
-  up.m_tiles = tiles_of(2 * w.ip, kExMTile), up.kb = tiles_of(H, 64), up.m = up.inner;
+  ExGemmParams up = gemm_params(a, w, d, 1, 2 * w.ip, pairs_for(a, rows, 2 * w.ip, H));
+  up.kb = tiles_of(H, 64), up.m = up.inner;
   up.act = act;
   up.gu = static_cast<__nv_bfloat16*>(gu);
   up.gu_vec = aligned(gu, 16) && I % 8 == 0;
-  ExGemmParams down = gemm_params(a, w, d, 1);
-  down.m_tiles = tiles_of(H, kExMTile), down.kb = tiles_of(I, 64), down.m = static_cast<int>(H);
+  ExGemmParams down = gemm_params(a, w, d, 1, H, pairs_for(a, rows, H, I));
+  down.kb = tiles_of(I, 64), down.m = static_cast<int>(H);
   rp.set(&down, ws);
   if (!map_up(&up.mapA, w_in, a, w) || !map_rows(&up, xp, H, rows, w.hp) ||
       !map3(&down.mapA, w_out, I, H, a->experts, w.ip, 128) || !map_rows(&down, act, I, rows, w.ip))
@@ -675,8 +692,8 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   g.weights = a->weights;
   g.wr = reinterpret_cast<float*>(ws + at_wr);
   MUON_TRY(c.run(launch_ex_gather(g, prows, kGatherBlocks * d.sms, stream)));
-  ExGemmParams da = gemm_params(a, w, d, kExSeg);
-  da.m_tiles = tiles_of(I, kExMTile), da.kb = tiles_of(H, 64), da.m = da.inner;
+  ExGemmParams da = gemm_params(a, w, d, kExSeg, I, 1);
+  da.kb = tiles_of(H, 64), da.m = da.inner;
   da.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));
   da.gu_vec = aligned(gu, 16) && I % 8 == 0;
   da.wr = g.wr, da.dgu = dgu, da.act = wact;
@@ -698,9 +715,9 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
     MUON_TRY(c.run(launch_ex_gather(g, prows, (beside ? 1 : kGatherBlocks) * d.sms, stream)));
   }
   if (dx) {
-    ExGemmParams p = gemm_params(a, w, d, kExSeg);
+    ExGemmParams p = gemm_params(a, w, d, kExSeg, H, pairs_for(a, prows, H, 2 * I));
     p.beside = beside;
-    p.m_tiles = tiles_of(H, kExMTile), p.kb = tiles_of(2 * w.ip, 64), p.m = static_cast<int>(H);
+    p.kb = tiles_of(2 * w.ip, 64), p.m = static_cast<int>(H);
     rp.set(&p, ws);
     if (!map_weights_mn(&p, w_in, H, 2 * w.ip, w.hp) || !map_rows(&p, dgu, 2 * w.ip, prows, gpitch))
       return MUON_ERR_CUDA;
@@ -710,13 +727,15 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   for (int k = 0; k < 2; ++k) {
     void* out = k ? dw_out : dw_in;
     if (!out) continue;
-    ExGemmParams p = gemm_params(a, w, d, kExSeg);
-    p.m = static_cast<int>(k ? H : 2 * w.ip), p.n = static_cast<int>(k ? I : H);
-    p.m_tiles = tiles_of(p.m, kExMTile), p.n_tiles = tiles_of(p.n, kExNTile);
+    const int64_t m = k ? H : 2 * w.ip;
+    ExGemmParams p = gemm_params(a, w, d, kExSeg, m, pairs_for(a, prows, m, prows / a->experts));
+    p.m = static_cast<int>(m), p.n = static_cast<int>(k ? I : H);
+    p.n_tiles = tiles_of(p.n, kExNTile);
     p.dw = out, p.dw_dt = dw_dt;
     p.dw_vec = aligned(out, 16) && p.n * esize(dw_dt) % 16 == 0;
     const int64_t ap = k ? xpitch : gpitch, bp = k ? apitch : xpitch;
-    if (!map_mn(&p.mapA, k ? dop : dgu, ap, prows, ap, 0) || !map_mn(&p.mapB, k ? wact : xp, bp, prows, bp, 0))
+    if (!map_mn(&p.mapA, k ? dop : dgu, ap, prows, ap, 0, 2) ||
+        !map_mn(&p.mapB, k ? wact : xp, bp, prows, bp, 0, 2 / p.pairs))
       return MUON_ERR_CUDA;
     MUON_TRY(c.run(launch_ex_gemm(k ? kExDwOut : kExDwIn, p, d.sms, false, stream)));
   }

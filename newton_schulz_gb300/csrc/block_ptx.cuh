@@ -82,6 +82,26 @@ __device__ __forceinline__ void tma_load_5d_pair(void* dst, const void* tmap, ui
       : "memory");
 }
 
+// As the pair loads, into the same place of every CTA of the cluster named in
+// cta_mask (this GPU's memory); each destination's pair completes its own
+// barrier at the offset of `bar`.
+__device__ __forceinline__ void tma_load_2d_pair_mc(void* dst, const void* tmap, uint32_t bar, int x, int y,
+                                                    uint16_t cta_mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "h"(cta_mask)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair_mc(void* dst, const void* tmap, uint32_t bar, int x, int y,
+                                                    int z, uint16_t cta_mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(cta_mask)
+      : "memory");
+}
+
 // As mbar_try_wait, suspended by the hardware for up to `ns` nanoseconds.
 __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar_addr, uint32_t parity, uint32_t ns) {
   uint32_t ok;

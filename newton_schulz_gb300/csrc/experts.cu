@@ -25,7 +25,7 @@
 //               16 bytes a thread straight into the stage took 0.5 us a stage
 //               against 0.39 from a copy of the rows in expert order, more than
 //               that copy costs;
-//   warp 1      TMEM; in the pair's CTA 0 it issues the MMAs of both;
+//   warp 1      TMEM; in a pair's CTA 0 it issues the MMAs of both;
 //   warps 2..9  epilogue, two sets of four (128 TMEM lanes each) that take
 //               the accumulator's column slabs in turn.
 // Two 256-column accumulators let the epilogue of a tile overlap the next
@@ -430,7 +430,7 @@ __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, c
       const uint32_t v = __shfl_sync(kFull, m[i], (w.lane >> 1) & 3);
       if ((w.lane >> 3) == i) e32 = (w.lane & 1) ? v >> 23 : (v >> 7) & 0xffu;
     }
-    if (c0 + w.lane < t.rows) ex[c0 * p.yep] = static_cast<uint8_t>(max(e32, kExpLeast));
+    if (c0 + w.lane < t.rows && w.m0 < p.m) ex[c0 * p.yep] = static_cast<uint8_t>(max(e32, kExpLeast));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 s;
@@ -654,8 +654,8 @@ __device__ __forceinline__ void epi_dw(const ExGemmParams& p, const Tile& t, con
 
 }  // namespace
 
-template <int KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
+template <int KIND, int PAIRS>
+__global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThreads, 1)
     ex_gemm_kernel(const __grid_constant__ ExGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -663,10 +663,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
   uint8_t* sStage = smem;
   uint8_t* sEpi = smem + kStages * kStageBytes;
   uint8_t* sBar = sEpi + 2 * set_bytes(KIND);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sBar);   // CTA 0's count for both
+  uint64_t* full = reinterpret_cast<uint64_t*>(sBar);   // a pair's CTA 0 counts for both
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;     // [2] accumulator ready
-  uint64_t* tempty = tfull + 2;          // [2] accumulator drained by both CTAs (CTA 0's)
+  uint64_t* tempty = tfull + 2;          // [2] accumulator drained by the pair (its CTA 0's)
   uint64_t* mma_drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -677,13 +677,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
   scan.tt = scan.poff + p.experts + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int crank = static_cast<int>(ptx::cluster_ctarank());
-  const int tile0 = static_cast<int>(blockIdx.x >> 1), tstep = static_cast<int>(gridDim.x >> 1);
+  const int rank = static_cast<int>(ptx::cluster_ctarank());
+  const int crank = rank & 1, pair = rank >> 1;      // place in the pair; pair of the cluster
+  const int tile0 = static_cast<int>(blockIdx.x) / (2 * PAIRS), tstep = static_cast<int>(gridDim.x) / (2 * PAIRS);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 1);
+      ptx::mbar_init(&empty[s], PAIRS);      // each pair's MMAs are done with it
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&tfull[b], 1);
@@ -702,12 +703,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
   if (warp == 2) scan_offsets(scan, p.experts, p.pad, KIND == kExDact, p.e0, p.e1, lane);
   ptx::tc_fence_before();
   __syncthreads();
-  ptx::cluster_sync();     // both CTAs' barriers are initialised
+  ptx::cluster_sync();     // every CTA's barriers are initialised
   ptx::tc_fence_after();
   ptx::launch_dependents();
   if (!p.beside) ptx::wait_dependency();
   const uint32_t tmem = *tmem_slot;
+  // tiles of the cluster: PAIRS M tiles and one column tile each
   const int tiles = is_dw(KIND) ? p.experts * p.m_tiles * p.n_tiles : scan.tt[p.experts] * p.m_tiles;
+  auto m_first = [&](const Tile& t) { return (t.m * PAIRS + pair) * kExMTile + crank * 128; };
 
   if (warp == 0) {
     // ---- TMA producer (lane 0; the others hold tiles) -----------------------------------
@@ -715,13 +718,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
     int stage = 0, issued = 0;
     uint32_t phase = 0;
     bool stop = false;
-    const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
+    const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), rank & ~1);
     for (int tile = tile0, it = 0; tile < tiles && !stop; tile += tstep, ++it) {
       const Tile t = feed.get(p, scan, tiles, tile0, tstep, it, lane);
-      // B: one box of 128 rows, or one or two of 32 for a small tile
-      const int half = t.cols / 2, boxes = half > 64 ? 0 : (half + 31) / 32;
-      const uint32_t bytes = 2 * (kOpBytes + (boxes ? boxes * 4096 : kOpBytes));
-      const int m0 = t.m * kExMTile + crank * 128;
+      // B: 128 rows in boxes of 128 / PAIRS, one from each pair for all; for a
+      // small tile one or two boxes of 32
+      const int half = t.cols / 2, small = half > 64 ? 0 : (half + 31) / 32;
+      const uint32_t bytes = 2 * (kOpBytes + (small ? small * 4096 : kOpBytes));
+      const int m0 = m_first(t);
+      const uint16_t mask = static_cast<uint16_t>(PAIRS == 2 ? 0x5 << crank : 0);
       for (int i = 0; lane == 0 && i < t.kb; ++i) {
         if (!wait_bounded(&empty[stage], phase ^ 1, abort_flag, p.status, p.timeout_ns, true)) {
           stop = true;
@@ -746,13 +751,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
           for (int h = 0; h < 2; ++h)
             ptx::tma_load_3d_pair(a + h * 8192, &p.mapA, bar, m0 + 64 * h, k, t.e);
         }
-        if (is_dw(KIND)) {
-          ptx::tma_load_3d_pair(b, &p.mapB, bar, 0, t.prow + k, t.n * 4 + crank * 2);
-        } else if (boxes == 0) {
-          ptx::tma_load_2d_pair(b, &p.mapB, bar, k, t.prow + crank * half);
-        } else {
-          for (int h = 0; h < boxes; ++h)
-            ptx::tma_load_2d_pair(b + h * 4096, &p.mapB32, bar, k, t.prow + crank * half + 32 * h);
+        if (PAIRS == 1) {
+          if (is_dw(KIND)) {
+            ptx::tma_load_3d_pair(b, &p.mapB, bar, 0, t.prow + k, t.n * 4 + crank * 2);
+          } else if (small == 0) {
+            ptx::tma_load_2d_pair(b, &p.mapB, bar, k, t.prow + crank * half);
+          } else {
+            for (int h = 0; h < small; ++h)
+              ptx::tma_load_2d_pair(b + h * 4096, &p.mapB32, bar, k, t.prow + crank * half + 32 * h);
+          }
+        } else if (is_dw(KIND)) {
+          ptx::tma_load_3d_pair_mc(b + pair * 8192, &p.mapB, bar, 0, t.prow + k, t.n * 4 + crank * 2 + pair, mask);
+        } else if (small == 0) {
+          ptx::tma_load_2d_pair_mc(b + pair * 8192, &p.mapB, bar, k, t.prow + crank * half + 64 * pair, mask);
+        } else if (pair < small) {
+          ptx::tma_load_2d_pair_mc(b + pair * 4096, &p.mapB32, bar, k, t.prow + crank * half + 32 * pair, mask);
         }
         ++issued;
         if (++stage == kStages) {
@@ -762,13 +775,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
       }
       stop = __shfl_sync(kFull, stop, 0);
     }
-    // CTA 0: the last copies of both CTAs have landed before the pair exits
+    // CTA 0: the last copies into both CTAs have landed before the pair exits
     if (crank == 0 && lane == 0)
       for (int j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
         wait_bounded(&full[j % kStages], (j / kStages) & 1, abort_flag, p.status, p.timeout_ns, false);
     __syncwarp();
   } else if (warp == 1) {
-    // ---- MMA issuer (CTA 0, lane 0; the others hold tiles) -------------------------------
+    // ---- MMA issuer (a pair's CTA 0, lane 0; the others hold tiles) -------------------------------
     if (crank == 0) {
       Feed<KIND> feed;
       int stage = 0, acc = 0;
@@ -809,20 +822,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
               ptx::umma_bf16_pair(d, a_hi | da, b_hi | db, idesc, acc_on);
               acc_on = 1;
             }
-            ptx::umma_commit_pair(&empty[stage], 0x3);
+            ptx::umma_commit_pair(&empty[stage], PAIRS == 1 ? 0x3 : 0xf);
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1;
             }
           }
-          ptx::umma_commit_pair(&tfull[buf], 0x3);
+          ptx::umma_commit_pair(&tfull[buf], static_cast<uint16_t>(0x3 << (2 * pair)));
         }
         ++acc;
         stop = __shfl_sync(kFull, stop, 0);
       }
       // no MMA may still run when TMEM is freed
       if (lane == 0) {
-        ptx::umma_commit_pair(mma_drain, 0x1);
+        ptx::umma_commit_pair(mma_drain, static_cast<uint16_t>(1 << rank));
         wait_bounded(mma_drain, 0, abort_flag, p.status, p.timeout_ns, false);
       }
     }
@@ -839,7 +852,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
     Feed<KIND> feed;
     for (int tile = tile0, it = 0; tile < tiles; tile += tstep, ++it) {
       const Tile t = feed.get(p, scan, tiles, tile0, tstep, it, lane);
-      w.m0 = t.m * kExMTile + crank * 128;
+      w.m0 = m_first(t);
       const int buf = acc & 1;
       w.taddr = tmem + buf * 256 + (static_cast<uint32_t>(w.q4 * 32) << 16);
       GateUp in;
@@ -866,7 +879,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBoundThreads, 1)
       if (t.kb > 0) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), 0));
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), rank & ~1));
         ++acc;
       }
     }
@@ -1023,15 +1036,39 @@ __global__ void __launch_bounds__(256)
 
 namespace {
 
-template <int KIND>
+// CTAs that are resident at once: clusters of four do not fill every GPC.
+template <int KIND, int PAIRS>
+int resident_ctas(int sms, int smem) {
+  if (PAIRS == 1) return sms / 2 * 2;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(sms / 4 * 4), c.blockDim = dim3(kThreads), c.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2 * PAIRS, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+  c.attrs = &at, c.numAttrs = 1;
+  int n = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, ex_gemm_kernel<KIND, PAIRS>, &c);
+  if (e != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    return sms / 4 * 4;      // the last clusters then start late
+  }
+  return n * 2 * PAIRS;
+}
+
+template <int KIND, int PAIRS>
 cudaError_t gemm_launch(ExGemmParams p, int sms, bool early, cudaStream_t s) {
   p.stages = kMostStages;
   if (gemm_smem(KIND, p.stages, p.experts) > kSmemLimit) p.stages = kMostStages - 1;
   const int smem = gemm_smem(KIND, p.stages, p.experts);
-  const cudaError_t e = cudaFuncSetAttribute(ex_gemm_kernel<KIND>,
+  const cudaError_t e = cudaFuncSetAttribute(ex_gemm_kernel<KIND, PAIRS>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_after(ex_gemm_kernel<KIND>, sms / 2 * 2, kThreads, smem, early, s, p);
+  return launch_after(ex_gemm_kernel<KIND, PAIRS>, resident_ctas<KIND, PAIRS>(sms, smem), kThreads, smem, early, s, p);
+}
+
+template <int KIND>
+cudaError_t gemm_pairs(const ExGemmParams& p, int sms, bool early, cudaStream_t s) {
+  return p.pairs == 2 ? gemm_launch<KIND, 2>(p, sms, early, s) : gemm_launch<KIND, 1>(p, sms, early, s);
 }
 
 unsigned some(int64_t n, int64_t most) { return static_cast<unsigned>(std::min(std::max<int64_t>(n, 1), most)); }
@@ -1040,12 +1077,12 @@ unsigned some(int64_t n, int64_t most) { return static_cast<unsigned>(std::min(s
 
 cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, bool early, cudaStream_t s) {
   switch (kind) {
-    case kExUp: return gemm_launch<kExUp>(p, sms, early, s);
-    case kExDown: return gemm_launch<kExDown>(p, sms, early, s);
-    case kExDact: return gemm_launch<kExDact>(p, sms, early, s);
-    case kExDx: return gemm_launch<kExDx>(p, sms, early, s);
-    case kExDwIn: return gemm_launch<kExDwIn>(p, sms, early, s);
-    default: return gemm_launch<kExDwOut>(p, sms, early, s);
+    case kExUp: return gemm_pairs<kExUp>(p, sms, early, s);
+    case kExDown: return gemm_pairs<kExDown>(p, sms, early, s);
+    case kExDact: return gemm_launch<kExDact, 1>(p, sms, early, s);
+    case kExDx: return gemm_pairs<kExDx>(p, sms, early, s);
+    case kExDwIn: return gemm_pairs<kExDwIn>(p, sms, early, s);
+    default: return gemm_pairs<kExDwOut>(p, sms, early, s);
   }
 }
 
