@@ -499,9 +499,11 @@ muon_status_t muon_route_backward(const muon_route_config_t *cfg, const void *lo
  *          hidden] it is a muon_group_t of whole matrices)
  *   w_out  bf16 [experts, hidden, inner]
  *   weights, offsets, src, pos   as muon_route_forward wrote them
- * Products accumulate in fp32; the activation and each slot's product are
- * rounded to bf16 once (they are the next product's operand and the sum's
- * terms).  out bf16 [tokens, hidden], row stride out_stride.
+ * Products accumulate in fp32; the activation is rounded to bf16 once (it is
+ * the next product's operand).  A slot's product, a term of the sum over slots
+ * (its weight comes after), is kept as 16-bit integers with one exponent per
+ * 32 columns, within 2^-15 of their largest magnitude, or in fp32 for a few
+ * rows.  out bf16 [tokens, hidden], row stride out_stride.
  * gu: bf16 [tokens * top_k, 2 * inner] or NULL: the gate and up values of
  * every row below offsets[experts], for muon_experts_backward (later rows
  * are not written).
@@ -530,8 +532,9 @@ muon_status_t muon_experts_forward(const muon_experts_t *args, void *out, int64_
  * dx bf16 [tokens, hidden] (row stride dx_stride); dw_in, dw_out shaped as
  * the weights, dtype dw_dtype (f32 or bf16); dweights f32 [tokens, top_k].
  * Any output may be NULL: not wanted.  Experts without rows get zero weight
- * gradients.  dgu and w a are rounded to bf16 once, as products' operands.
- * No sum's order depends on timing. */
+ * gradients.  dgu and w a are rounded to bf16 once, as products' operands;
+ * dx's terms are kept as the forward's slot products are.  No sum's order
+ * depends on timing. */
 muon_status_t muon_experts_backward(const muon_experts_t *args, const void *dout,
                                     int64_t dout_stride, const void *gu, void *dx,
                                     int64_t dx_stride, void *dw_in, void *dw_out,

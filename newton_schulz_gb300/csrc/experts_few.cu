@@ -4,7 +4,10 @@
 // one column of out over all of a token's slots, 16 bytes a lane and load.
 // One token through 8 of 256 experts of [768, 2048] (75 MB): the tile kernels
 // took 34 us on 48 and 64 of their 76 CTA pairs' tiles, without the copy and
-// the sum over slots that they need besides.
+// the sum over slots that they need besides; these two take 21.
+// The activation is rounded to bf16 as the tile kernels' operand is: in fp32
+// its reads, every warp's of the second kernel, took 2 us of that more (the
+// error of out against 64 bits 0.0017 instead of 0.0024 in norm).
 #include "block.h"
 #include "block_ptx.cuh"
 
