@@ -105,6 +105,7 @@ struct RouteParams {
   int32_t* idx;
   float* weights;
   int experts, top_k, score, groups, top_groups, group_score, renorm;
+  int vec, bias_vec;              // 16-byte aligned rows of logits, bias
   float scale;
   unsigned* status;
 };
@@ -117,6 +118,7 @@ struct RouteGradParams {
   const float* dweights;
   void* dlogits;
   int experts, top_k, score, renorm;
+  int vec, dvec;                  // 16-byte aligned rows of logits, dlogits
   float scale;
 };
 

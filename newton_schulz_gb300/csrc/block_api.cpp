@@ -236,6 +236,7 @@ muon_status_t route_impl(const muon_route_config_t* cfg, const void* logits, int
   p.bias = bias, p.mask = mask, p.idx = idx, p.weights = weights;
   p.experts = cfg->experts, p.top_k = cfg->top_k, p.score = cfg->score, p.groups = cfg->groups;
   p.top_groups = cfg->top_groups, p.group_score = cfg->group_score, p.renorm = cfg->renormalize != 0;
+  p.vec = l.rows16(), p.bias_vec = aligned(bias, 16);
   p.scale = cfg->scale;
   p.status = d.status;
   PlanParams pp = plan_params(idx, tokens, cfg->top_k, cfg->experts, offsets, src, pos);
@@ -300,6 +301,7 @@ muon_status_t route_grad_impl(const muon_route_config_t* cfg, const void* logits
   p.idx = idx, p.dweights = dweights, p.dlogits = dlogits;
   p.experts = cfg->experts, p.top_k = cfg->top_k, p.score = cfg->score;
   p.renorm = cfg->renormalize != 0;
+  p.vec = l.rows16(), p.dvec = o.rows16();
   p.scale = cfg->scale;
   std::lock_guard<std::mutex> lock(api_mutex());
   Counter c;

@@ -102,6 +102,13 @@ __device__ __forceinline__ void tma_load_3d_pair_mc(void* dst, const void* tmap,
       : "memory");
 }
 
+// Largest of the full warp's floats (no NaN among them).
+__device__ __forceinline__ float redux_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
 // As mbar_try_wait, suspended by the hardware for up to `ns` nanoseconds.
 __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar_addr, uint32_t parity, uint32_t ns) {
   uint32_t ok;

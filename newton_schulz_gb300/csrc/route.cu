@@ -1,11 +1,13 @@
 // Routing of tokens to experts: scores, group cut, top-k, weights; the stable
 // counting sort of the chosen (token, slot) pairs by expert; the gradient.
 //
-// One warp takes one token; expert e sits in lane e % 32, register e / 32.
-// A key becomes an unsigned word whose order is the float's (0: not to be
-// chosen), so a maximum over the warp is one redux instruction, and the
-// lowest expert among equal keys another.  Bound by instruction issue and
-// latency: a token's 4 * experts bytes are little against its top_k rounds.
+// One warp takes one token; lane l holds experts l * EPL .. l * EPL + EPL - 1 in
+// registers (EPL experts a lane, a power of two), so a row is read 16 bytes a
+// lane, a group of experts is a run of lanes, and the lowest expert among equal
+// keys is in the lowest lane that a vote names.  A maximum over the warp is one
+// redux instruction on the keys as floats (-inf: not to be chosen).  Bound by
+// instruction issue: a token's 4 * experts bytes are little against its scores
+// and its top_k rounds.
 #include <type_traits>
 
 #include "block.h"
@@ -18,14 +20,6 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRouteWarps = 8;
 
-__device__ __forceinline__ uint32_t ordered(float f) {
-  const uint32_t b = __float_as_uint(f + 0.f);   // -0 becomes +0: equal keys tie
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float unordered(uint32_t u) {
-  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
@@ -37,26 +31,100 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// x[i] = logit of expert i * 32 + lane, -inf where there is none or it is
-// not finite; returns whether a NaN or +inf was met.
-template <int EPL>
-__device__ __forceinline__ bool load_logits(float (&x)[EPL], const void* base, int dtype,
-                                            int64_t off, int experts, int lane) {
-  bool bad = false;
+// v[i] = element i of this lane's EPL elements at `at`, `fill` from the n-th on.
+// vec: 16-byte aligned where a lane's share is 16 bytes or more (by its size below).
+template <int EPL, typename T>
+__device__ __forceinline__ void load_share(float (&v)[EPL], const T* at, int n, float fill, bool vec) {
+  constexpr int kBytes = EPL * sizeof(T);
+  auto value = [](uint32_t w, int half) {
+    return sizeof(T) == 4 ? __uint_as_float(w) : __uint_as_float(half ? w & 0xffff0000u : w << 16);
+  };
+  constexpr int kPer = 4 / sizeof(T);      // elements a word
+  if (kBytes >= 4 && vec && n >= EPL) {
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int c = 0; c < kBytes / 16; ++c) {
+        const uint4 q = reinterpret_cast<const uint4*>(at)[c];
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4 * kPer; ++i) v[c * 4 * kPer + i] = value(w[i / kPer], i % kPer);
+      }
+    } else if constexpr (kBytes == 8) {
+      const uint2 q = *reinterpret_cast<const uint2*>(at);
+      const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = value(w[i / kPer], i % kPer);
+    } else if constexpr (kBytes == 4) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(at);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = value(w, i % kPer);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = i * 32 + lane;
-    x[i] = -INFINITY;
-    if (e < experts) {
-      x[i] = dtype == kDtF32
-                 ? static_cast<const float*>(base)[off + e]
-                 : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[off + e]);
-      if (!(x[i] < INFINITY)) {
-        x[i] = -INFINITY;
-        bad = true;
-      }
+    v[i] = fill;
+    if (i < n) {
+      if constexpr (sizeof(T) == 4) v[i] = at[i];
+      else v[i] = __bfloat162float(at[i]);
     }
   }
+}
+
+// As load_share, to memory.
+template <int EPL, typename T>
+__device__ __forceinline__ void store_share(T* at, const float (&v)[EPL], int n, bool vec) {
+  constexpr int kWords = EPL * sizeof(T) / 4;
+  if (kWords > 0 && vec && n >= EPL) {
+    uint32_t w[kWords > 0 ? kWords : 1];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = __float_as_uint(v[i]);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    if constexpr (kWords >= 4) {
+#pragma unroll
+      for (int c = 0; c < kWords / 4; ++c)
+        reinterpret_cast<uint4*>(at)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    } else if constexpr (kWords == 2) {
+      *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+    } else {
+      *reinterpret_cast<uint32_t*>(at) = w[0];
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (i < n) {
+      if constexpr (sizeof(T) == 4) at[i] = v[i];
+      else at[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+// x[i] = logit of expert lane * EPL + i as read, -inf where there is none.
+template <int EPL>
+__device__ __forceinline__ void load_logits(float (&x)[EPL], const void* base, int dtype, int64_t row,
+                                            int experts, bool vec, int lane) {
+  const int first = lane * EPL;
+  if (dtype == kDtF32)
+    load_share<EPL>(x, static_cast<const float*>(base) + row + first, experts - first, -INFINITY, vec);
+  else
+    load_share<EPL>(x, static_cast<const __nv_bfloat16*>(base) + row + first, experts - first, -INFINITY, vec);
+}
+// NaN and +inf become -inf; returns whether one was met.
+template <int EPL>
+__device__ __forceinline__ bool only_finite(float (&x)[EPL]) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (!(x[i] < INFINITY)) {
+      x[i] = -INFINITY;
+      bad = true;
+    }
   return bad;
 }
 
@@ -77,7 +145,8 @@ __device__ __forceinline__ float softmax_parts(const float (&x)[EPL], float (&e)
   return warp_sum(sum);
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+// the quotient within 2 units of the last place
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
 
 }  // namespace
 
@@ -91,102 +160,110 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
   int32_t my_idx = -1;
   float my_score = 0.f;
   if (!p.mask || p.mask[tok]) {
-    float x[EPL], sc[EPL];
-    if (load_logits<EPL>(x, p.logits, p.dtype, tok * p.stride, p.experts, lane))
-      atomicOr(p.status, kDevNonfinite);
+    const int first = lane * EPL;
+    float x[EPL], sc[EPL], key[EPL];
+    load_logits<EPL>(x, p.logits, p.dtype, tok * p.stride, p.experts, p.vec, lane);
+    if (p.bias) load_share<EPL>(key, p.bias + first, p.experts - first, 0.f, p.bias_vec);
+    if (only_finite<EPL>(x)) atomicOr(p.status, kDevNonfinite);
     // every expert's score, where the choice goes by scores
-    const bool by_score = p.bias != nullptr || (p.top_groups < p.groups && p.group_score == 1);
+    const bool cut = p.top_groups < p.groups, sum2 = p.group_score == 1;
+    const bool by_score = p.bias != nullptr || (cut && sum2);
     float top = 0.f, sum = 0.f;
     if (p.score == 0) {
       sum = softmax_parts<EPL>(x, sc, &top);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) sc[i] = sum > 0.f ? sc[i] / sum : 0.f;
+      for (int i = 0; i < EPL; ++i) sc[i] *= inv;
     } else if (by_score) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) sc[i] = sigmoid(x[i]);
     }
-    uint32_t key[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = i * 32 + lane;
-      const bool alive = x[i] > -INFINITY;
-      const float v = p.bias ? sc[i] + (alive ? p.bias[e] : 0.f) : x[i];
-      key[i] = alive && v > -INFINITY ? ordered(v) : 0u;
+      const float v = p.bias ? sc[i] + key[i] : x[i];
+      key[i] = x[i] > -INFINITY && v > -INFINITY ? v : -INFINITY;      // a NaN of the bias: not chosen
     }
-    if (p.top_groups < p.groups) {
+    if (cut) {
       const int per = p.experts / p.groups;
-      const bool sum2 = p.group_score == 1;
-      // what a group is ranked by, as ordered words
-      uint32_t rank[EPL];
+      const bool own = sum2 && !p.bias;      // groups ranked by scores, the choice by logits
+      auto rank = [&](int i) { return own && key[i] > -INFINITY ? sc[i] : key[i]; };
+      // a, b: the two largest of a group
+      auto score_of = [&](float a, float b) { return sum2 && b > -INFINITY ? a + b : a; };
+      const int run = per / EPL;             // lanes a group
+      if (per % EPL == 0 && (run & (run - 1)) == 0) {
+        float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) rank[i] = sum2 && !p.bias && key[i] ? ordered(sc[i]) : key[i];
-      uint32_t best[2] = {0u, 0u};     // this lane: groups lane and 32 + lane
-      // a: this lane's largest in the group, b: its second largest
-      auto score_of = [&](uint32_t a, uint32_t b) {
-        const uint32_t m1 = __reduce_max_sync(kFull, a);
-        if (!sum2 || !m1) return m1;
-        const int owner = __ffs(__ballot_sync(kFull, a == m1)) - 1;
-        const uint32_t m2 = __reduce_max_sync(kFull, lane == owner ? b : a);
-        return ordered(m2 ? unordered(m1) + unordered(m2) : unordered(m1));
-      };
-      uint64_t keep = 0;
-      if (per == 32) {
-        // register i is group i
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (i < p.groups) {
-            const uint32_t score = score_of(rank[i], 0u);
-            if (lane == i) best[0] = score;
+        for (int i = 0; i < EPL; ++i) {
+          const float v = rank(i);
+          b = fmaxf(b, fminf(a, v));
+          a = fmaxf(a, v);
+        }
+        for (int o = 1; o < run; o <<= 1) {
+          const float oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
+          b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+          a = fmaxf(a, oa);
+        }
+        float left = score_of(a, b);         // the same in every lane of the group
+        bool kept = false;
+        for (int j = 0; j < p.top_groups; ++j) {
+          const float m = ptx::redux_max(left);
+          if (!(m > -INFINITY)) break;
+          const int at = __ffs(__ballot_sync(kFull, left == m)) - 1;
+          if (((lane ^ at) & ~(run - 1)) == 0) {
+            kept = true;
+            left = -INFINITY;
           }
+        }
+        if (!kept) {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) key[i] = -INFINITY;
+        }
       } else {
+        float best[2] = {-INFINITY, -INFINITY};      // this lane: groups lane and 32 + lane
         for (int g = 0; g < p.groups; ++g) {
-          uint32_t a = 0u, b = 0u;
+          float a = -INFINITY, b = -INFINITY;
 #pragma unroll
           for (int i = 0; i < EPL; ++i) {
-            const int e = i * 32 + lane - g * per;
-            const uint32_t v = e >= 0 && e < per ? rank[i] : 0u;
-            b = max(b, min(a, v));
-            a = max(a, v);
+            const int e = first + i - g * per;
+            const float v = e >= 0 && e < per ? rank(i) : -INFINITY;
+            b = fmaxf(b, fminf(a, v));
+            a = fmaxf(a, v);
           }
-          const uint32_t score = score_of(a, b);
+          const float m1 = ptx::redux_max(a);
+          const int owner = __ffs(__ballot_sync(kFull, a == m1)) - 1;
+          const float score = score_of(m1, sum2 ? ptx::redux_max(lane == owner ? b : a) : -INFINITY);
           if (lane == (g & 31)) {
             if (g < 32) best[0] = score;
             else best[1] = score;
           }
         }
-      }
-      for (int j = 0; j < p.top_groups; ++j) {
-        const uint32_t m = __reduce_max_sync(kFull, max(best[0], best[1]));
-        if (!m) break;
-        const unsigned lo = __ballot_sync(kFull, best[0] == m), hi = __ballot_sync(kFull, best[1] == m);
-        const int g = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
-        keep |= 1ull << g;
-        if (lane == (g & 31)) {
-          if (g < 32) best[0] = 0u;
-          else best[1] = 0u;
+        uint64_t keep = 0;
+        for (int j = 0; j < p.top_groups; ++j) {
+          const float m = ptx::redux_max(fmaxf(best[0], best[1]));
+          if (!(m > -INFINITY)) break;
+          const unsigned lo = __ballot_sync(kFull, best[0] == m), hi = __ballot_sync(kFull, best[1] == m);
+          const int g = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
+          keep |= 1ull << g;
+          if (lane == (g & 31)) {
+            if (g < 32) best[0] = -INFINITY;
+            else best[1] = -INFINITY;
+          }
         }
-      }
-      if (per == 32) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-          if (!((keep >> i) & 1)) key[i] = 0u;
-      } else {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const int e = i * 32 + lane;
-          if (e < p.experts && !((keep >> (e / per)) & 1)) key[i] = 0u;
-        }
+          if (first + i < p.experts && !((keep >> ((first + i) / per)) & 1)) key[i] = -INFINITY;
       }
     }
     // this lane's two largest keys, lower experts first among equal ones: a lane
     // is looked through again only when it gives its third expert
-    uint32_t a = 0u, a2 = 0u, used = 0u;
+    float a = -INFINITY, a2 = -INFINITY;
+    uint32_t used = 0u;
     int at = 0, at2 = 0;
     auto rescan = [&] {
-      a = a2 = 0u;
+      a = a2 = -INFINITY;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const uint32_t v = (used >> i) & 1u ? 0u : key[i];
+        const float v = (used >> i) & 1u ? -INFINITY : key[i];
         if (v > a) {
           a2 = a;
           at2 = at;
@@ -201,15 +278,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     rescan();
     bool second = true;      // a2 is the next after a
     for (int j = 0; j < k; ++j) {
-      const uint32_t m = __reduce_max_sync(kFull, a);
-      if (!m) break;
-      const unsigned who = __ballot_sync(kFull, a == m);
-      int owner = __ffs(who) - 1;
-      int e = __shfl_sync(kFull, at, owner) * 32 + owner;
-      if (who & (who - 1)) {      // equal keys in several lanes
-        e = static_cast<int>(__reduce_min_sync(kFull, a == m ? static_cast<uint32_t>(at * 32 + lane) : ~0u));
-        owner = e & 31;
-      }
+      const float m = ptx::redux_max(a);
+      if (!(m > -INFINITY)) break;
+      const int owner = __ffs(__ballot_sync(kFull, a == m)) - 1;
+      const int e = owner * EPL + __shfl_sync(kFull, at, owner);
       if (lane == j) my_idx = e;
       if (lane == owner) {
         used |= 1u << at;
@@ -248,7 +320,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   const int64_t tok = blockIdx.x * static_cast<int64_t>(kRouteWarps) + (threadIdx.x >> 5);
   if (tok >= p.tokens) return;
   float x[EPL], sc[EPL], d[EPL];
-  load_logits<EPL>(x, p.logits, p.dtype, tok * p.stride, p.experts, lane);
+  load_logits<EPL>(x, p.logits, p.dtype, tok * p.stride, p.experts, p.vec, lane);
+  only_finite<EPL>(x);
   if (p.score == 0) {
     float top;
     const float sum = softmax_parts<EPL>(x, sc, &top);
@@ -266,21 +339,23 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     dw = p.dweights[tok * p.top_k + lane] * p.scale;
   }
   // each chosen expert's dweight to its lane and register, through shared memory
-  __shared__ float s_d[kRouteWarps][EPL * 32];
+  constexpr int kPitch = EPL + (EPL >= 4 ? 4 : 1);      // lanes' words in different banks
+  __shared__ __align__(16) float s_d[kRouteWarps][32 * kPitch];
   __shared__ uint32_t s_chosen[kRouteWarps][32];
   const int warp = threadIdx.x >> 5;
+  float* mine = &s_d[warp][lane * kPitch];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) s_d[warp][i * 32 + lane] = 0.f;
+  for (int i = 0; i < EPL; ++i) mine[i] = 0.f;
   s_chosen[warp][lane] = 0u;
   __syncwarp();
   if (e >= 0 && e < p.experts) {
-    s_d[warp][e] = dw;
-    atomicOr(&s_chosen[warp][e & 31], 1u << (e >> 5));
+    s_d[warp][e / EPL * kPitch + e % EPL] = dw;
+    atomicOr(&s_chosen[warp][e / EPL], 1u << (e % EPL));
   }
   __syncwarp();
-  const uint32_t chosen = s_chosen[warp][lane];    // bit i: expert i * 32 + lane is chosen
+  const uint32_t chosen = s_chosen[warp][lane];    // bit i: expert lane * EPL + i is chosen
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) d[i] = s_d[warp][i * 32 + lane];
+  for (int i = 0; i < EPL; ++i) d[i] = mine[i];
   if (p.renorm) {
     float total = 0.f, dot = 0.f;
 #pragma unroll
@@ -303,16 +378,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     sub = warp_sum(sub);
   }
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int ei = i * 32 + lane;
-    if (ei >= p.experts) continue;
+  for (int i = 0; i < EPL; ++i)
     // renormalised softmax: sum over the chosen of d q is zero, so the full
     // softmax's slope is q d as well
-    const float g = p.score == 0 ? sc[i] * (d[i] - sub) : d[i] * sc[i] * (1.f - sc[i]);
-    const int64_t at = tok * p.dstride + ei;
-    if (p.dtype == kDtF32) static_cast<float*>(p.dlogits)[at] = g;
-    else static_cast<__nv_bfloat16*>(p.dlogits)[at] = __float2bfloat16_rn(g);
-  }
+    d[i] = p.score == 0 ? sc[i] * (d[i] - sub) : d[i] * sc[i] * (1.f - sc[i]);
+  const int first = lane * EPL;
+  const int64_t at = tok * p.dstride + first;
+  if (p.dtype == kDtF32) store_share<EPL>(static_cast<float*>(p.dlogits) + at, d, p.experts - first, p.dvec);
+  else store_share<EPL>(static_cast<__nv_bfloat16*>(p.dlogits) + at, d, p.experts - first, p.dvec);
 }
 
 // ---- plan ------------------------------------------------------------------------------------
