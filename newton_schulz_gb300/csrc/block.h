@@ -135,8 +135,8 @@ struct PlanParams {
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t s);
 cudaError_t launch_route_grad(const RouteGradParams& p, cudaStream_t s);
-cudaError_t launch_plan_hist(const PlanParams& p, cudaStream_t s);
-cudaError_t launch_plan(const PlanParams& p, bool early, cudaStream_t s);   // early: see launch_after
+cudaError_t launch_plan_hist(const PlanParams& p, bool early, cudaStream_t s);   // early: see launch_after
+cudaError_t launch_plan(const PlanParams& p, bool early, cudaStream_t s);
 
 // ---- experts' products ---------------------------------------------------------------------
 // Products on the tensor cores (experts.cu), by operand and result.

@@ -182,8 +182,8 @@ bool unsupported_route(int64_t tokens, int top_k, int experts, int groups) {
 
 // The plan's launches; hist: workspace, unused with one tile.
 muon_status_t plan_launches(const PlanParams& p, Counter* c, cudaStream_t stream) {
-  if (p.tiles > 1) MUON_TRY(c->run(launch_plan_hist(p, stream)));
-  return c->run(launch_plan(p, c->n > 0 && p.tiles == 1, stream));
+  if (p.tiles > 1) MUON_TRY(c->run(launch_plan_hist(p, c->n > 0, stream)));
+  return c->run(launch_plan(p, c->n > 0, stream));
 }
 
 PlanParams plan_params(const int32_t* idx, int64_t tokens, int top_k, int experts, int32_t* offsets,

@@ -404,7 +404,9 @@ __device__ __forceinline__ int expert_of(const PlanParams& p, int64_t entry, int
 // hist[tile][e]: entries of expert e among the tile's tokens.
 __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(const __grid_constant__ PlanParams p) {
   extern __shared__ int s_cnt[];
+  ptx::launch_dependents();
   for (int e = threadIdx.x; e < p.experts; e += kPlanThreads) s_cnt[e] = 0;
+  ptx::wait_dependency();
   __syncthreads();
   const int64_t total = p.tokens * p.top_k;
   const int64_t first = blockIdx.x * static_cast<int64_t>(kPlanTokens) * p.top_k;
@@ -455,13 +457,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       if (p.tiles == 1) {
         for (int w = 0; w < kPlanWarps; ++w) all += start[w * E + e];
       } else {
-        for (int b0 = 0; b0 < p.tiles; b0 += 16) {      // 16 loads in flight
-          int c[16];
+        for (int b0 = 0; b0 < p.tiles; b0 += 32) {      // 32 loads in flight
+          int c[32];
 #pragma unroll
-          for (int b = 0; b < 16; ++b)
+          for (int b = 0; b < 32; ++b)
             c[b] = b0 + b < p.tiles ? p.hist[static_cast<int64_t>(b0 + b) * E + e] : 0;
 #pragma unroll
-          for (int b = 0; b < 16; ++b) {
+          for (int b = 0; b < 32; ++b) {
             all += c[b];
             if (b0 + b < static_cast<int>(blockIdx.x)) before += c[b];
           }
@@ -500,9 +502,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
   }
   __syncthreads();
+  int next = expert_of(p, w0 + lane, w1);
   for (int64_t i0 = w0; i0 < w1; i0 += 32) {
     const int64_t i = i0 + lane;
-    const int e = expert_of(p, i, w1);
+    const int e = next;
+    next = expert_of(p, i + 32, w1);
     const unsigned peers = __match_any_sync(kFull, e);
     int row = -1;
     if (e >= 0) row = start[warp * E + e] + __popc(peers & ((1u << lane) - 1u));
@@ -549,9 +553,8 @@ cudaError_t launch_route_grad(const RouteGradParams& p, cudaStream_t s) {
   });
 }
 
-cudaError_t launch_plan_hist(const PlanParams& p, cudaStream_t s) {
-  plan_hist_kernel<<<p.tiles, kPlanThreads, p.experts * sizeof(int), s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_plan_hist(const PlanParams& p, bool early, cudaStream_t s) {
+  return launch_after(plan_hist_kernel, p.tiles, kPlanThreads, p.experts * sizeof(int), early, s, p);
 }
 
 cudaError_t launch_plan(const PlanParams& p, bool early, cudaStream_t s) {
