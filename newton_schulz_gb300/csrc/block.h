@@ -186,7 +186,7 @@ struct ExGemmParams {
 };
 
 // Rows of x (or dout) of experts [e0, e1) in expert order, zero rows up to each segment's end.
-struct ExGatherParams {
+struct ExSpreadParams {
   const __nv_bfloat16* x;
   int64_t xs;
   __nv_bfloat16* out;             // [padded rows][hp]
@@ -194,9 +194,10 @@ struct ExGatherParams {
   const float* weights;           // with wr: the row's weight
   float* wr;
   const int32_t* offsets;
-  const int32_t* src;
-  int64_t rows, hidden, hp;
+  const int32_t* pos;
+  int64_t tokens, rows, hidden, hp;
   int experts, top_k, pad, e0, e1;
+  int span;                       // columns a warp takes at a time (set at the launch)
 };
 
 struct ExCombineParams {          // out[t] = sum_j w[t,j] y[pos[t,j]]
@@ -241,7 +242,7 @@ cudaError_t launch_ex_few(const ExFewParams& p, cudaStream_t s);    // two launc
 
 // early: see launch_after
 cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, bool early, cudaStream_t s);
-cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, int blocks, cudaStream_t s);
+cudaError_t launch_ex_spread(ExSpreadParams p, int blocks, cudaStream_t s);
 cudaError_t launch_ex_combine(const ExCombineParams& p, int sms, bool early, cudaStream_t s);
 cudaError_t launch_ex_dweights(const ExWeightParams& p, cudaStream_t s);
 // mats matrices [rows][cols] -> [rows_p][cols_p], zeros around

@@ -509,13 +509,13 @@ ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const Api
   return p;
 }
 
-ExGatherParams gather_params(const muon_experts_t* a, const WeightPlan& w, int pad) {
-  ExGatherParams g;
+ExSpreadParams spread_params(const muon_experts_t* a, const WeightPlan& w, int pad) {
+  ExSpreadParams g;
   std::memset(&g, 0, sizeof(g));
   g.x = static_cast<const __nv_bfloat16*>(a->x), g.xs = a->x_stride;
   g.e0 = 0, g.e1 = a->experts;
-  g.offsets = a->offsets, g.src = a->src;
-  g.rows = a->tokens * a->top_k, g.hidden = a->hidden, g.hp = w.hp;
+  g.offsets = a->offsets, g.pos = a->pos;
+  g.tokens = a->tokens, g.rows = a->tokens * a->top_k, g.hidden = a->hidden, g.hp = w.hp;
   g.experts = a->experts, g.top_k = a->top_k, g.pad = pad;
   return g;
 }
@@ -546,7 +546,7 @@ struct RowPlan {
   }
 };
 
-constexpr int kGatherBlocks = 5;      // per SM, for a copy that runs alone
+constexpr int kSpreadBlocks = 5;      // per SM, for a copy that runs alone
 constexpr int64_t kBesideRows = 16384;      // from here a copy takes longer than its overlap costs
 
 // Many rows: the copy of the first experts' rows runs alone, that of the rest
@@ -607,16 +607,16 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   const __nv_bfloat16 *w_in, *w_out;
   MUON_TRY(pack_weights(a, w, ws, &w_in, &w_out, &c, stream));
   const bool early = rows <= 4096;      // short kernels
-  ExGatherParams g = gather_params(a, w, 1);
+  ExSpreadParams g = spread_params(a, w, 1);
   g.out = xp;
   g.vec = v.x.rows16();
   const int part = beside_part(a);
   if (part) {
     g.e1 = part;
-    MUON_TRY(c.run(launch_ex_gather(g, rows, kGatherBlocks * d.sms, stream)));
+    MUON_TRY(c.run(launch_ex_spread(g, kSpreadBlocks * d.sms, stream)));
     g.e0 = part, g.e1 = a->experts;
   }
-  MUON_TRY(c.run(launch_ex_gather(g, rows, (part ? 1 : kGatherBlocks) * d.sms, stream)));
+  MUON_TRY(c.run(launch_ex_spread(g, (part ? 1 : kSpreadBlocks) * d.sms, stream)));
   ExGemmParams up = gemm_params(a, w, d, 1, 2 * w.ip, pairs_for(a, rows, 2 * w.ip, H));
   up.kb = tiles_of(H, 64), up.m = up.inner;
   up.act = act;
@@ -687,13 +687,13 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   Counter c;
   const __nv_bfloat16 *w_in, *w_out;
   MUON_TRY(pack_weights(a, w, ws, &w_in, &w_out, &c, stream));
-  ExGatherParams g = gather_params(a, w, kExSeg);
+  ExSpreadParams g = spread_params(a, w, kExSeg);
   g.hp = xpitch;
   g.x = static_cast<const __nv_bfloat16*>(dout), g.xs = dos, g.out = dop;
   g.vec = vd.rows16();
   g.weights = a->weights;
   g.wr = reinterpret_cast<float*>(ws + at_wr);
-  MUON_TRY(c.run(launch_ex_gather(g, prows, kGatherBlocks * d.sms, stream)));
+  MUON_TRY(c.run(launch_ex_spread(g, kSpreadBlocks * d.sms, stream)));
   ExGemmParams da = gemm_params(a, w, d, kExSeg, I, 1);
   da.kb = tiles_of(H, 64), da.m = da.inner;
   da.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));
@@ -714,7 +714,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
     g.x = static_cast<const __nv_bfloat16*>(a->x), g.xs = a->x_stride, g.out = xp;
     g.vec = v.x.rows16();
     g.wr = nullptr;
-    MUON_TRY(c.run(launch_ex_gather(g, prows, (beside ? 1 : kGatherBlocks) * d.sms, stream)));
+    MUON_TRY(c.run(launch_ex_spread(g, (beside ? 1 : kSpreadBlocks) * d.sms, stream)));
   }
   if (dx) {
     ExGemmParams p = gemm_params(a, w, d, kExSeg, H, pairs_for(a, prows, H, 2 * I));

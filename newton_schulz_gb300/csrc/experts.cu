@@ -892,10 +892,10 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThread
   if (p.beside) ptx::wait_dependency();      // this kernel's end is also that one's
 }
 
-// Copies the rows of x (or dout) into expert order, a warp per row, eight
-// 16-byte loads a lane in flight and the next row's token with them; HBM-bound
-// (every row of x is read top_k times, from L2 while x fits there).
-__global__ void __launch_bounds__(256, 5) ex_gather_kernel(const __grid_constant__ ExGatherParams p) {
+// Copies the rows of x (or dout) into expert order: a warp reads a token's
+// columns once, eight 16-byte loads a lane in flight and the next token's rows
+// with them, and writes them to each of its rows.  HBM-bound.
+__global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant__ ExSpreadParams p) {
   extern __shared__ int s_scan[];
   Scan s;
   s.off = s_scan;
@@ -907,43 +907,50 @@ __global__ void __launch_bounds__(256, 5) ex_gather_kernel(const __grid_constant
   __syncthreads();
   if (threadIdx.x < 32) scan_offsets(s, p.experts, p.pad, false, 0, 0, lane);
   __syncthreads();
-  const int total = s.poff[p.e1];
-  const int step = gridDim.x * 8;
-  // token * top_k + slot of a padded row, -1 where there is none
-  auto source = [&](int r) {
-    if (r >= total) return -1;
-    int urow = r;
-    if (p.pad > 1) {
-      const int e = find(s.poff, p.experts, r);
-      urow = s.off[e] + r - s.poff[e];
-      if (urow >= s.off[e + 1]) return -1;
-    }
-    const int32_t v = p.src[urow];
-    return v < p.rows ? v : -1;
+  const int lo = s.off[p.e0], hi = s.off[p.e1];
+  const int step = gridDim.x * 8, first = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int begin = blockIdx.y * p.span, end = min(begin + p.span, static_cast<int>(p.hp));
+  const int tokens = static_cast<int>(p.tokens), hidden = static_cast<int>(p.hidden);
+  // row of this lane's slot of a token
+  auto slot = [&](int64_t tok) {
+    return tok < tokens && lane < p.top_k ? p.pos[tok * p.top_k + lane] : -1;
   };
-  int r = s.poff[p.e0] + blockIdx.x * 8 + (threadIdx.x >> 5);
-  int sv = source(r);
-  for (; r < total; r += step) {
-    const int next = source(r + step);
-    const int64_t tok = sv < 0 ? 0 : sv / p.top_k;
-    {
-      const __nv_bfloat16* in = p.x + tok * p.xs;
-      __nv_bfloat16* out = p.out + r * p.hp;
-      for (int64_t c0 = lane * 8; c0 < p.hp; c0 += 2048) {
-        uint4 v[8];
+  int next = slot(first);
+  for (int64_t tok = first; tok < tokens; tok += step) {
+    int row = next >= lo && next < hi ? next : -1;
+    next = slot(tok + step);
+    const unsigned live = __ballot_sync(kFull, row >= 0);
+    if (!live) continue;
+    if (p.pad > 1 && row >= 0) {
+      const int e = find(s.off, p.experts, row);
+      row += s.poff[e] - s.off[e];
+    }
+    const __nv_bfloat16* in = p.x + tok * p.xs;
+    for (int cb = begin; cb < end; cb += 2048) {
+      const int c0 = cb + lane * 8;
+      uint4 v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t c = c0 + 256 * j;
-          v[j] = load8(in + c, sv < 0 ? 0 : static_cast<int>(min(p.hidden - c, static_cast<int64_t>(8))),
-                       p.vec != 0);
-        }
+      for (int j = 0; j < 8; ++j) {
+        const int c = c0 + 256 * j;
+        v[j] = load8(in + c, c < end ? min(hidden - c, 8) : 0, p.vec != 0);
+      }
+      for (unsigned m = live; m; m &= m - 1) {
+        __nv_bfloat16* out = p.out + __shfl_sync(kFull, row, __ffs(m) - 1) * p.hp;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (c0 + 256 * j < p.hp) *reinterpret_cast<uint4*>(out + c0 + 256 * j) = v[j];
+          if (c0 + 256 * j < end) *reinterpret_cast<uint4*>(out + c0 + 256 * j) = v[j];
       }
     }
-    if (p.wr && lane == 0) p.wr[r] = sv < 0 ? 0.f : p.weights[sv];
-    sv = next;
+    if (p.wr && row >= 0 && begin == 0) p.wr[row] = p.weights[tok * p.top_k + lane];
+  }
+  if (p.pad == 1) return;
+  // zeros after each expert's rows
+  for (int i = first; i < (p.e1 - p.e0) * p.pad; i += step) {
+    const int e = p.e0 + i / p.pad, r = s.poff[e] + s.off[e + 1] - s.off[e] + i % p.pad;
+    if (r >= s.poff[e + 1]) continue;
+    for (int c = begin + lane * 8; c < end; c += 256)
+      *reinterpret_cast<uint4*>(p.out + r * p.hp + c) = make_uint4(0u, 0u, 0u, 0u);
+    if (p.wr && lane == 0 && begin == 0) p.wr[r] = 0.f;
   }
 }
 
@@ -1086,13 +1093,17 @@ cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, bool early,
   }
 }
 
-cudaError_t launch_ex_gather(const ExGatherParams& p, int64_t padded_rows, int blocks, cudaStream_t s) {
+cudaError_t launch_ex_spread(ExSpreadParams p, int blocks, cudaStream_t s) {
   // the products' split of the SM's memory: an SM changes it only when idle, and
   // a product is to start beside this kernel
-  const cudaError_t e = cudaFuncSetAttribute(ex_gather_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+  const cudaError_t e = cudaFuncSetAttribute(ex_spread_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                              cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
-  ex_gather_kernel<<<some((padded_rows + 7) / 8, blocks), 256, 3 * (p.experts + 1) * sizeof(int), s>>>(p);
+  // few tokens: more warps, each with one load a lane
+  p.span = p.tokens >= int64_t{4} * blocks ? 2048 : 256;
+  const unsigned pieces = static_cast<unsigned>((p.hp + p.span - 1) / p.span);
+  const dim3 grid(some((p.tokens + 7) / 8, std::max(1, blocks / static_cast<int>(pieces))), pieces);
+  ex_spread_kernel<<<grid, 256, 3 * (p.experts + 1) * sizeof(int), s>>>(p);
   return cudaGetLastError();
 }
 
