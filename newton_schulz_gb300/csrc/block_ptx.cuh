@@ -122,9 +122,11 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar_addr, uint32_t pa
   return ok != 0;
 }
 
-// Arrive on an mbarrier given by its cluster address.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrive on an mbarrier given by its cluster address, without ordering memory:
+// it frees accumulator columns whose loads are complete (tcgen05.wait and
+// fence), and a release would first wait for the tile's stores to land.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // 16 lanes x 32 (x4) or 16 (x2) 32-bit columns.  Thread t holds, per 8

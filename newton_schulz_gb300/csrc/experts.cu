@@ -879,7 +879,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThread
       if (t.kb > 0) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), rank & ~1));
+        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), rank & ~1));
         ++acc;
       }
     }
