@@ -30,7 +30,11 @@
 //               the accumulator's column slabs in turn.
 // Two 256-column accumulators let the epilogue of a tile overlap the next
 // tile's products.  Bound by the tensor cores where experts have hundreds of
-// rows, by HBM (every weight read once) where they have a few.
+// rows, by HBM (every weight read once) where they have a few.  4093 tokens
+// through 2 of 8 x [14336, 4096]: up 1094 us, down 586 (1.76 and 1.64 PFLOP/s);
+// 48 tokens through 8 of 256 x [768, 2048]: 225 us for 1.38 GB of weights, 0.90
+// of the measured copy rate; 8192 tokens' gradient through 8 of 64 x
+// [768, 2048]: dact 196, dx 298 (with x's copy beside it), dw_in 264, dw_out 155.
 //
 // The tile list follows from the offsets on the device: every CTA scans them
 // (one warp, a few hundred cycles), so the host needs no counts.  Offsets are
@@ -894,7 +898,8 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThread
 
 // Copies the rows of x (or dout) into expert order: a warp reads a token's
 // columns once, eight 16-byte loads a lane in flight and the next token's rows
-// with them, and writes them to each of its rows.  HBM-bound.
+// with them, and writes them to each of its rows.  HBM-bound: 65536 rows of 2048
+// in 54 us (5.6 TB/s); 77 with a warp per row, which reads a token top_k times.
 __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant__ ExSpreadParams p) {
   extern __shared__ int s_scan[];
   Scan s;
@@ -957,7 +962,8 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
 // out[t] = sum over slots, in slot order, a block per token, eight columns a
 // lane, SLOTS slots' loads in flight and the next token's rows with them;
 // HBM-bound once the conversions are few (two fp32 operations an instruction, no
-// branch per slot: a slot without a row reads row 0 with weight 0).
+// branch per slot: a slot without a row reads row 0 with weight 0): 16384 tokens
+// of 8 slots of 2048 in 92 us, 6.3 TB/s.
 template <int SLOTS>
 __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constant__ ExCombineParams p) {
   const int lane = threadIdx.x & 31;

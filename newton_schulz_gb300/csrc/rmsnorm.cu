@@ -12,6 +12,11 @@
 // reciprocal root and the codes' factor are CUDA's approximate ones (within 2
 // units of the last place): with 256 threads a row, exact divisions by each of
 // them were a fifth of the instructions.
+//
+// Of the measured copy rate: 16384 x 8192 bf16 with a residual 172 us, 0.92
+// (a ring of bulk copies 184 us); its gradient at 16384 x 4096 80 us, 0.98, and
+// 4 us for the gains' sums; 4099 x 2048 into e4m3 per 128 columns 19 us, 0.71:
+// the codes' conversions and two reductions a row show there.
 #include <cuda_fp8.h>
 
 #include <algorithm>

