@@ -158,7 +158,6 @@ struct ExGemmParams {
   const int32_t* offsets;         // [experts + 1]
   int64_t rows;                   // tokens * top_k, the most rows there are
   int experts;
-  int e0, e1;                     // experts of this launch (kExDw*: all)
   int beside;                     // 1: runs beside the previous launch, whose results it does not use
   int pad;                        // padded row numbering: segments of 1 or kExSeg rows
   int m_tiles, n_tiles;           // M tiles of a pair; kExDw*: N tiles
@@ -185,7 +184,7 @@ struct ExGemmParams {
   unsigned long long timeout_ns;
 };
 
-// Rows of x (or dout) of experts [e0, e1) in expert order, zero rows up to each segment's end.
+// Rows of x (or dout) in expert order, zero rows up to each segment's end.
 struct ExSpreadParams {
   const __nv_bfloat16* x;
   int64_t xs;
@@ -196,7 +195,7 @@ struct ExSpreadParams {
   const int32_t* offsets;
   const int32_t* pos;
   int64_t tokens, rows, hidden, hp;
-  int experts, top_k, pad, e0, e1;
+  int experts, top_k, pad;
   int span;                       // columns a warp takes at a time (set at the launch)
 };
 

@@ -499,7 +499,6 @@ ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const Api
   p.offsets = a->offsets;
   p.rows = a->tokens * a->top_k;
   p.experts = a->experts;
-  p.e0 = 0, p.e1 = a->experts;
   p.pad = pad;
   p.pairs = pairs;
   p.m_tiles = tiles_of(m_rows, kExMTile * pairs);
@@ -513,7 +512,6 @@ ExSpreadParams spread_params(const muon_experts_t* a, const WeightPlan& w, int p
   ExSpreadParams g;
   std::memset(&g, 0, sizeof(g));
   g.x = static_cast<const __nv_bfloat16*>(a->x), g.xs = a->x_stride;
-  g.e0 = 0, g.e1 = a->experts;
   g.offsets = a->offsets, g.pos = a->pos;
   g.tokens = a->tokens, g.rows = a->tokens * a->top_k, g.hidden = a->hidden, g.hp = w.hp;
   g.experts = a->experts, g.top_k = a->top_k, g.pad = pad;
@@ -547,16 +545,6 @@ struct RowPlan {
 };
 
 constexpr int kSpreadBlocks = 5;      // per SM, for a copy that runs alone
-constexpr int64_t kBesideRows = 16384;      // from here a copy takes longer than its overlap costs
-
-// Many rows: the copy of the first experts' rows runs alone, that of the rest
-// while the first experts' product runs (the copy needs HBM, the product the
-// tensor cores; one block an SM leaves it room).  The number of experts in the
-// first part, or 0: one copy, one product.  16384 tokens over 256 experts of
-// [768, 2048]: 1265 -> 1220 us.
-int beside_part(const muon_experts_t* a) {
-  return a->tokens * a->top_k >= kBesideRows && a->experts >= 8 ? a->experts / 3 : 0;
-}
 
 muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, void* gu, cudaStream_t stream) {
   ExpertsViews v;
@@ -610,13 +598,7 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   ExSpreadParams g = spread_params(a, w, 1);
   g.out = xp;
   g.vec = v.x.rows16();
-  const int part = beside_part(a);
-  if (part) {
-    g.e1 = part;
-    MUON_TRY(c.run(launch_ex_spread(g, kSpreadBlocks * d.sms, stream)));
-    g.e0 = part, g.e1 = a->experts;
-  }
-  MUON_TRY(c.run(launch_ex_spread(g, (part ? 1 : kSpreadBlocks) * d.sms, stream)));
+  MUON_TRY(c.run(launch_ex_spread(g, kSpreadBlocks * d.sms, stream)));
   ExGemmParams up = gemm_params(a, w, d, 1, 2 * w.ip, pairs_for(a, rows, 2 * w.ip, H));
   up.kb = tiles_of(H, 64), up.m = up.inner;
   up.act = act;
@@ -628,11 +610,6 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   if (!map_up(&up.mapA, w_in, a, w) || !map_rows(&up, xp, H, rows, w.hp) ||
       !map3(&down.mapA, w_out, I, H, a->experts, w.ip, 128) || !map_rows(&down, act, I, rows, w.ip))
     return MUON_ERR_CUDA;
-  if (part) {
-    up.e1 = part, up.beside = 1;
-    MUON_TRY(c.run(launch_ex_gemm(kExUp, up, d.sms, true, stream)));
-    up.e0 = part, up.e1 = a->experts, up.beside = 0;
-  }
   MUON_TRY(c.run(launch_ex_gemm(kExUp, up, d.sms, early, stream)));
   MUON_TRY(c.run(launch_ex_gemm(kExDown, down, d.sms, early, stream)));
   MUON_TRY(c.run(launch_ex_combine(combine_params(a, down, a->weights, o), d.sms, early, stream)));
@@ -708,8 +685,12 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
     const ExWeightParams wp{da.part, a->pos, dweights, rows, parts};
     MUON_TRY(c.run(launch_ex_dweights(wp, stream)));
   }
-  // x's rows, for dw_in: with many rows their copy runs beside dx's product
-  const bool beside = dx && dw_in && rows >= kBesideRows;
+  // x's rows, for dw_in: with many rows their copy runs while dx's product does (it
+  // needs HBM, the product the tensor cores; one block an SM leaves it room).
+  // 8192 tokens over 64 experts of [768, 2048]: 1094 -> 1080 us; with fewer the
+  // copy is over before the overlap pays.  Cutting the forward's copy and first
+  // product in two to do the same: 1104 -> 1114 us on 16384 tokens over 256.
+  const bool beside = dx && dw_in && rows >= 16384;
   if (dw_in) {
     g.x = static_cast<const __nv_bfloat16*>(a->x), g.xs = a->x_stride, g.out = xp;
     g.vec = v.x.rows16();

@@ -98,9 +98,7 @@ __device__ __forceinline__ void fetch_offsets(const Scan& s, const int32_t* offs
     s.off[e] = max(0, static_cast<int>(min(static_cast<int64_t>(offsets[e]), rows)));
 }
 
-// Experts outside [e0, e1) get no row tiles.
-__device__ __forceinline__ void scan_offsets(const Scan& s, int experts, int pad, bool tile_pads, int e0, int e1,
-                                             int lane) {
+__device__ __forceinline__ void scan_offsets(const Scan& s, int experts, int pad, bool tile_pads, int lane) {
   int top = 0, pbase = 0, tbase = 0;
   for (int eb = 0; eb <= experts; eb += 32) {
     const int e = eb + lane;
@@ -119,7 +117,7 @@ __device__ __forceinline__ void scan_offsets(const Scan& s, int experts, int pad
     const int e = eb + lane;
     const int cnt = e < experts ? s.off[e + 1] - s.off[e] : 0;
     const int pc = round_up(cnt, pad);
-    const int nt = e >= e0 && e < e1 ? ((tile_pads ? pc : cnt) + kExNTile - 1) / kExNTile : 0;
+    const int nt = ((tile_pads ? pc : cnt) + kExNTile - 1) / kExNTile;
     int a = pc, b = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -704,7 +702,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThread
   if (warp == 1) ptx::tmem_alloc_pair(tmem_slot, kTmemCols);
   fetch_offsets(scan, p.offsets, p.experts, p.rows);
   __syncthreads();
-  if (warp == 2) scan_offsets(scan, p.experts, p.pad, KIND == kExDact, p.e0, p.e1, lane);
+  if (warp == 2) scan_offsets(scan, p.experts, p.pad, KIND == kExDact, lane);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();     // every CTA's barriers are initialised
@@ -910,9 +908,9 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
   ptx::launch_dependents();
   fetch_offsets(s, p.offsets, p.experts, p.rows);
   __syncthreads();
-  if (threadIdx.x < 32) scan_offsets(s, p.experts, p.pad, false, 0, 0, lane);
+  if (threadIdx.x < 32) scan_offsets(s, p.experts, p.pad, false, lane);
   __syncthreads();
-  const int lo = s.off[p.e0], hi = s.off[p.e1];
+  const int total = s.off[p.experts];
   const int step = gridDim.x * 8, first = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int begin = blockIdx.y * p.span, end = min(begin + p.span, static_cast<int>(p.hp));
   const int tokens = static_cast<int>(p.tokens), hidden = static_cast<int>(p.hidden);
@@ -922,7 +920,7 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
   };
   int next = slot(first);
   for (int64_t tok = first; tok < tokens; tok += step) {
-    int row = next >= lo && next < hi ? next : -1;
+    int row = next < total ? next : -1;
     next = slot(tok + step);
     const unsigned live = __ballot_sync(kFull, row >= 0);
     if (!live) continue;
@@ -950,8 +948,8 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
   }
   if (p.pad == 1) return;
   // zeros after each expert's rows
-  for (int i = first; i < (p.e1 - p.e0) * p.pad; i += step) {
-    const int e = p.e0 + i / p.pad, r = s.poff[e] + s.off[e + 1] - s.off[e] + i % p.pad;
+  for (int i = first; i < p.experts * p.pad; i += step) {
+    const int e = i / p.pad, r = s.poff[e] + s.off[e + 1] - s.off[e] + i % p.pad;
     if (r >= s.poff[e + 1]) continue;
     for (int c = begin + lane * 8; c < end; c += 256)
       *reinterpret_cast<uint4*>(p.out + r * p.hp + c) = make_uint4(0u, 0u, 0u, 0u);
