@@ -30,15 +30,16 @@ void api_set_launches(int n);
 // Launch of a kernel that follows another of the same call.  early: it may
 // start while that one ends (programmatic dependent launch), and waits for its
 // results with ptx::wait_dependency before it touches what the call's kernels
-// share.  That saves 2 to 3 us a launch where the kernels are short (one token
-// through the experts' products 26.8 -> 21.3 us); under long ones the waiting
+// share.  That saves 2 to 4 us a launch where the kernels are short (one token
+// through the experts' products 26.8 -> 21.3 us, 7 tokens' gradient in eight
+// launches 89 -> 52); under long ones the waiting
 // blocks take room from the running ones (the products' gradient over 64
 // experts 1247 -> 1266 us).
 template <typename... A>
-cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned block, size_t smem, bool early,
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, unsigned block, size_t smem, bool early,
                          cudaStream_t s, typename std::common_type<A>::type... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -197,6 +198,7 @@ struct ExSpreadParams {
   int64_t tokens, rows, hidden, hp;
   int experts, top_k, pad;
   int span;                       // columns a warp takes at a time (set at the launch)
+  int beside;                     // 1: runs beside the previous launch, whose results it does not use
 };
 
 struct ExCombineParams {          // out[t] = sum_j w[t,j] y[pos[t,j]]
@@ -243,7 +245,7 @@ cudaError_t launch_ex_few(const ExFewParams& p, cudaStream_t s);    // two launc
 cudaError_t launch_ex_gemm(int kind, const ExGemmParams& p, int sms, bool early, cudaStream_t s);
 cudaError_t launch_ex_spread(ExSpreadParams p, int blocks, cudaStream_t s);
 cudaError_t launch_ex_combine(const ExCombineParams& p, int sms, bool early, cudaStream_t s);
-cudaError_t launch_ex_dweights(const ExWeightParams& p, cudaStream_t s);
+cudaError_t launch_ex_dweights(const ExWeightParams& p, bool early, cudaStream_t s);
 // mats matrices [rows][cols] -> [rows_p][cols_p], zeros around
 cudaError_t launch_ex_repack(const __nv_bfloat16* in, int64_t mats, int64_t rows, int64_t cols,
                              __nv_bfloat16* out, int64_t rows_p, int64_t cols_p, cudaStream_t s);

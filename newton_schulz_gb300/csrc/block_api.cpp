@@ -544,6 +544,7 @@ struct RowPlan {
   }
 };
 
+constexpr int64_t kEarlyRows = 4096;  // most rows whose kernels are short: see launch_after
 constexpr int kSpreadBlocks = 5;      // per SM, for a copy that runs alone
 
 muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, void* gu, cudaStream_t stream) {
@@ -594,7 +595,7 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   __nv_bfloat16* act = reinterpret_cast<__nv_bfloat16*>(ws + at_act);
   const __nv_bfloat16 *w_in, *w_out;
   MUON_TRY(pack_weights(a, w, ws, &w_in, &w_out, &c, stream));
-  const bool early = rows <= 4096;      // short kernels
+  const bool early = rows <= kEarlyRows;
   ExSpreadParams g = spread_params(a, w, 1);
   g.out = xp;
   g.vec = v.x.rows16();
@@ -671,32 +672,37 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   g.weights = a->weights;
   g.wr = reinterpret_cast<float*>(ws + at_wr);
   MUON_TRY(c.run(launch_ex_spread(g, kSpreadBlocks * d.sms, stream)));
+  // x's rows, for dw_in, are copied beside something: with many rows while dx's
+  // product runs (the copy needs HBM, the product the tensor cores; one block an
+  // SM leaves it room), else while dout's are.  8192 tokens over 64 experts of
+  // [768, 2048]: 1094 -> 1080 us.  Cutting the forward's copy and first product
+  // in two to do the same: 1104 -> 1114 us on 16384 tokens over 256.
+  const bool many = rows >= 16384, beside = dx && dw_in && many;
+  const bool early = rows <= kEarlyRows;
+  auto copy_x = [&](int blocks, bool with_previous) {
+    g.x = static_cast<const __nv_bfloat16*>(a->x), g.xs = a->x_stride, g.out = xp;
+    g.vec = v.x.rows16();
+    g.wr = nullptr;
+    g.beside = with_previous;
+    return c.run(launch_ex_spread(g, blocks * d.sms, stream));
+  };
+  float* const wr = g.wr;
+  if (dw_in && !beside) MUON_TRY(copy_x(kSpreadBlocks, true));
   ExGemmParams da = gemm_params(a, w, d, kExSeg, I, 1);
   da.kb = tiles_of(H, 64), da.m = da.inner;
   da.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));
   da.gu_vec = aligned(gu, 16) && I % 8 == 0;
-  da.wr = g.wr, da.dgu = dgu, da.act = wact;
+  da.wr = wr, da.dgu = dgu, da.act = wact;
   da.ap = static_cast<int>(apitch), da.gp = static_cast<int>(gpitch);
   da.part = reinterpret_cast<float*>(ws + at_part);
   if (!map_weights_mn(&da, w_out, I, H, w.ip) || !map_rows(&da, dop, H, prows, xpitch))
     return MUON_ERR_CUDA;
-  MUON_TRY(c.run(launch_ex_gemm(kExDact, da, d.sms, false, stream)));
+  MUON_TRY(c.run(launch_ex_gemm(kExDact, da, d.sms, early, stream)));
   if (dweights) {
     const ExWeightParams wp{da.part, a->pos, dweights, rows, parts};
-    MUON_TRY(c.run(launch_ex_dweights(wp, stream)));
+    MUON_TRY(c.run(launch_ex_dweights(wp, early, stream)));
   }
-  // x's rows, for dw_in: with many rows their copy runs while dx's product does (it
-  // needs HBM, the product the tensor cores; one block an SM leaves it room).
-  // 8192 tokens over 64 experts of [768, 2048]: 1094 -> 1080 us; with fewer the
-  // copy is over before the overlap pays.  Cutting the forward's copy and first
-  // product in two to do the same: 1104 -> 1114 us on 16384 tokens over 256.
-  const bool beside = dx && dw_in && rows >= 16384;
-  if (dw_in) {
-    g.x = static_cast<const __nv_bfloat16*>(a->x), g.xs = a->x_stride, g.out = xp;
-    g.vec = v.x.rows16();
-    g.wr = nullptr;
-    MUON_TRY(c.run(launch_ex_spread(g, (beside ? 1 : kSpreadBlocks) * d.sms, stream)));
-  }
+  if (beside) MUON_TRY(copy_x(1, false));
   if (dx) {
     ExGemmParams p = gemm_params(a, w, d, kExSeg, H, pairs_for(a, prows, H, 2 * I));
     p.beside = beside;
@@ -704,8 +710,8 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
     rp.set(&p, ws);
     if (!map_weights_mn(&p, w_in, H, 2 * w.ip, w.hp) || !map_rows(&p, dgu, 2 * w.ip, prows, gpitch))
       return MUON_ERR_CUDA;
-    MUON_TRY(c.run(launch_ex_gemm(kExDx, p, d.sms, beside, stream)));
-    MUON_TRY(c.run(launch_ex_combine(combine_params(a, p, nullptr, ox), d.sms, false, stream)));
+    MUON_TRY(c.run(launch_ex_gemm(kExDx, p, d.sms, beside || early, stream)));
+    MUON_TRY(c.run(launch_ex_combine(combine_params(a, p, nullptr, ox), d.sms, early, stream)));
   }
   for (int k = 0; k < 2; ++k) {
     void* out = k ? dw_out : dw_in;
@@ -720,7 +726,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
     if (!map_mn(&p.mapA, k ? dop : dgu, ap, prows, ap, 0, 2) ||
         !map_mn(&p.mapB, k ? wact : xp, bp, prows, bp, 0, 2 / p.pairs))
       return MUON_ERR_CUDA;
-    MUON_TRY(c.run(launch_ex_gemm(k ? kExDwOut : kExDwIn, p, d.sms, false, stream)));
+    MUON_TRY(c.run(launch_ex_gemm(k ? kExDwOut : kExDwIn, p, d.sms, early, stream)));
   }
   api_set_launches(c.n);
   return MUON_OK;

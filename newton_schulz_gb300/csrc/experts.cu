@@ -946,15 +946,15 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
     }
     if (p.wr && row >= 0 && begin == 0) p.wr[row] = p.weights[tok * p.top_k + lane];
   }
-  if (p.pad == 1) return;
   // zeros after each expert's rows
-  for (int i = first; i < p.experts * p.pad; i += step) {
+  for (int i = first; p.pad > 1 && i < p.experts * p.pad; i += step) {
     const int e = i / p.pad, r = s.poff[e] + s.off[e + 1] - s.off[e] + i % p.pad;
     if (r >= s.poff[e + 1]) continue;
     for (int c = begin + lane * 8; c < end; c += 256)
       *reinterpret_cast<uint4*>(p.out + r * p.hp + c) = make_uint4(0u, 0u, 0u, 0u);
     if (p.wr && lane == 0 && begin == 0) p.wr[r] = 0.f;
   }
+  if (p.beside) ptx::wait_dependency();      // this kernel's end is also that one's
 }
 
 // out[t] = sum over slots, in slot order, a block per token, eight columns a
@@ -1107,8 +1107,7 @@ cudaError_t launch_ex_spread(ExSpreadParams p, int blocks, cudaStream_t s) {
   p.span = p.tokens >= int64_t{4} * blocks ? 2048 : 256;
   const unsigned pieces = static_cast<unsigned>((p.hp + p.span - 1) / p.span);
   const dim3 grid(some((p.tokens + 7) / 8, std::max(1, blocks / static_cast<int>(pieces))), pieces);
-  ex_spread_kernel<<<grid, 256, 3 * (p.experts + 1) * sizeof(int), s>>>(p);
-  return cudaGetLastError();
+  return launch_after(ex_spread_kernel, grid, 256, 3 * (p.experts + 1) * sizeof(int), p.beside != 0, s, p);
 }
 
 cudaError_t launch_ex_combine(const ExCombineParams& p, int sms, bool early, cudaStream_t s) {
@@ -1120,8 +1119,8 @@ cudaError_t launch_ex_combine(const ExCombineParams& p, int sms, bool early, cud
   return launch_after(ex_combine_kernel<8>, grid, block, 0, early, s, p);
 }
 
-cudaError_t launch_ex_dweights(const ExWeightParams& p, cudaStream_t s) {
-  return launch_after(ex_dweights_kernel, some((p.rows + 255) / 256, 1 << 16), 256, 0, false, s, p);
+cudaError_t launch_ex_dweights(const ExWeightParams& p, bool early, cudaStream_t s) {
+  return launch_after(ex_dweights_kernel, some((p.rows + 255) / 256, 1 << 16), 256, 0, early, s, p);
 }
 
 cudaError_t launch_ex_repack(const __nv_bfloat16* in, int64_t mats, int64_t rows, int64_t cols,
