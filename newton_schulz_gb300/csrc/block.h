@@ -32,9 +32,8 @@ void api_set_launches(int n);
 // results with ptx::wait_dependency before it touches what the call's kernels
 // share.  That saves 2 to 4 us a launch where the kernels are short (one token
 // through the experts' products 26.8 -> 21.3 us, 7 tokens' gradient in eight
-// launches 89 -> 52); under long ones the waiting
-// blocks take room from the running ones (the products' gradient over 64
-// experts 1247 -> 1266 us).
+// launches 89 -> 52); under long ones the waiting blocks take room from the
+// running ones (the products' gradient over 64 experts 1247 -> 1266 us).
 template <typename... A>
 cudaError_t launch_after(void (*kernel)(A...), dim3 grid, unsigned block, size_t smem, bool early,
                          cudaStream_t s, typename std::common_type<A>::type... args) {

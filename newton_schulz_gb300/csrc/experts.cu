@@ -395,9 +395,9 @@ __device__ __forceinline__ void epi_up(const ExGemmParams& p, const Tile& t, con
 // per row and 32 features (a warp's lanes): q = v * 2^(13 - e), e the exponent of
 // the piece's largest value.  The error, 2^-15 of that largest value, is far below
 // the bf16 rounding of the sum, where bf16 rows would add as much again, and
-// half of fp32's bytes are written and read (16384 tokens over
-// 256 x [768, 2048], product and sum: 398 + 167 us with fp32 rows, 378 + 91 so).  A piece that holds an
-// infinity or NaN is NaN.
+// half of fp32's bytes are written and read (16384 tokens over 256 x [768, 2048],
+// product and sum: 398 + 167 us with fp32 rows, 378 + 91 so).  A piece that holds
+// an infinity or NaN is NaN.
 __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
   const int orow = w.tid >> 4, chunk = w.tid & 15, h = w.m0 + chunk * 8;
   int16_t* const y = p.y + static_cast<int64_t>(t.urow + orow) * p.yp + h;
