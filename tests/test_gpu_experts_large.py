@@ -1,6 +1,6 @@
 """The experts' products where their launches take another form: clusters of
-two CTA pairs (256 rows an expert and 1024 of K or more), row copies beside
-the products (16384 rows over 8 experts or more), and the border between the
+two CTA pairs (256 rows an expert and 1024 of K or more), a row copy beside
+the gradient's product (16384 rows or more), and the border between the
 matrix-vector products of a few rows and the tiles.  Against the formulas in
 64 bits, an expert at a time.
 
