@@ -3,6 +3,7 @@
 // their kernels.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -169,7 +170,7 @@ struct ExGemmParams {
   __nv_bfloat16* act;             // [padded rows][ap]: kExUp act, kExDact w a
   __nv_bfloat16* gu;              // [rows][2 inner]: kExUp output or null, kExDact input
   int gu_vec;                     // 16-byte accesses to gu are legal
-  int16_t* y;                     // [rows][yp] scaled integers
+  __half* y;                      // [rows][yp] values scaled by a power of two
   int64_t yp;
   uint8_t* yexp;                  // [rows][yep] exponents, one per 32 columns
   int64_t yep;
@@ -201,7 +202,7 @@ struct ExSpreadParams {
 };
 
 struct ExCombineParams {          // out[t] = sum_j w[t,j] y[pos[t,j]]
-  const int16_t* y;               // as ExGemmParams wrote it
+  const __half* y;                // as ExGemmParams wrote it
   int64_t yp;
   const uint8_t* yexp;
   int64_t yep;

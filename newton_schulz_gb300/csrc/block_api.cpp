@@ -539,7 +539,7 @@ struct RowPlan {
     at_e = c->take(rows * yep);
   }
   void set(ExGemmParams* p, char* ws) const {
-    p->y = reinterpret_cast<int16_t*>(ws + at_y), p->yp = yp;
+    p->y = reinterpret_cast<__half*>(ws + at_y), p->yp = yp;
     p->yexp = reinterpret_cast<uint8_t*>(ws + at_e), p->yep = yep;
   }
 };

@@ -47,6 +47,8 @@
 // rows with zeros: the weight gradients' K blocks then end with their
 // expert's, and no row of another expert, nor anything unwritten, is ever
 // multiplied.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "block.h"
@@ -69,7 +71,7 @@ constexpr int kBoundThreads = 480;
 constexpr uint32_t kTmemCols = 512;
 constexpr unsigned kFull = 0xffffffffu;
 // least exponent of a piece of rows: its factors both ways are normal numbers
-constexpr uint32_t kExpLeast = 14;
+constexpr uint32_t kExpLeast = 15;
 
 constexpr bool is_dw(int kind) { return kind == kExDwIn || kind == kExDwOut; }
 constexpr bool a_mn(int kind) { return kind >= kExDact; }   // A read MN-major
@@ -270,6 +272,11 @@ __device__ __forceinline__ float2 sigmoid2(float2 g) { return make_float2(sigmoi
 __device__ __forceinline__ float2 f2(uint32_t lo, uint32_t hi) { return make_float2(f(lo), f(hi)); }
 __device__ __forceinline__ float2 f2(uint32_t pair) { return make_float2(lo_of(pair), hi_of(pair)); }
 __device__ __forceinline__ uint32_t pack(float2 v) { return pack(v.x, v.y); }
+__device__ __forceinline__ uint32_t pack_half(float2 v) {
+  const __half2 h = __float22half2_rn(v);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 of_half(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 
 // 8 bf16 at p[0..8), of which the first n exist.
 __device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int n, bool vec) {
@@ -391,16 +398,19 @@ __device__ __forceinline__ void epi_up(const ExGemmParams& p, const Tile& t, con
   }
 }
 
-// Rows for the sum over slots, as 16-bit integers (plus 2^15) with one exponent
-// per row and 32 features (a warp's lanes): q = v * 2^(13 - e), e the exponent of
-// the piece's largest value.  The error, 2^-15 of that largest value, is far below
-// the bf16 rounding of the sum, where bf16 rows would add as much again, and
-// half of fp32's bytes are written and read (16384 tokens over 256 x [768, 2048],
-// product and sum: 398 + 167 us with fp32 rows, 378 + 91 so).  A piece that holds
-// an infinity or NaN is NaN.
+// Rows for the sum over slots, as 16-bit floats (IEEE half) with one exponent
+// per row and 32 features (a warp's lanes): q = v * 2^(14 - e), e the exponent of
+// the piece's largest value.  A value keeps 11 bits while it is above 2^-28 of
+// that largest one (below, its error is 2^-39 of it): a term errs by at most 2^-11
+// of itself, an eighth of what the bf16 operand behind it and the bf16 result
+// add, whatever its neighbours hold.  (15-bit integers, uniform in a piece, gave a
+// feature beside one 1000 times larger an error of 2.6 %; bf16 rows would add as
+// much as the result's rounding.)  Half of fp32's bytes are written and read
+// (16384 tokens over 256 x [768, 2048], product and sum: 398 + 167 us with fp32
+// rows, 378 + 91 with 16 bits).  A piece that holds an infinity or NaN is NaN.
 __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
   const int orow = w.tid >> 4, chunk = w.tid & 15, h = w.m0 + chunk * 8;
-  int16_t* const y = p.y + static_cast<int64_t>(t.urow + orow) * p.yp + h;
+  __half* const y = p.y + static_cast<int64_t>(t.urow + orow) * p.yp + h;
   uint8_t* const ex = p.yexp + static_cast<int64_t>(t.urow + w.lane) * p.yep + (w.m0 >> 5) + w.q4;
   const bool mine = h < p.yp;
   const uint32_t out = staged(w.stg, orow, chunk, 256);     // row + 8 keeps row % 8
@@ -436,17 +446,14 @@ __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, c
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 s;
-      s.x = f((267u - min(max((m[i] >> 7) & 0xffu, kExpLeast), 254u)) << 23);
-      s.y = f((267u - min(max(m[i] >> 23, kExpLeast), 254u)) << 23);
-      // adding 2^23 + 2^15 leaves the rounded integer plus 2^15 in the low bits
-      const float2 big = make_float2(8421376.f, 8421376.f);
+      s.x = f((268u - min(max((m[i] >> 7) & 0xffu, kExpLeast), 254u)) << 23);
+      s.y = f((268u - min(max(m[i] >> 23, kExpLeast), 254u)) << 23);
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t* v = &r[b][4 * i + 2 * q];
-          const float2 x = ptx::fma2(f2(v[0], v[1]), s, big);
-          v[0] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x5410);
+          v[0] = pack_half(ptx::mul2(f2(v[0], v[1]), s));
         }
     }
 #pragma unroll
@@ -958,10 +965,9 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
 }
 
 // out[t] = sum over slots, in slot order, a block per token, eight columns a
-// lane, SLOTS slots' loads in flight and the next token's rows with them;
-// HBM-bound once the conversions are few (two fp32 operations an instruction, no
-// branch per slot: a slot without a row reads row 0 with weight 0): 16384 tokens
-// of 8 slots of 2048 in 92 us, 6.3 TB/s.
+// lane, SLOTS slots' loads in flight and the next token's rows with them (a slot
+// without a row loads nothing and counts as zeros); HBM-bound once the conversions
+// are few: 16384 tokens of 8 slots of 2048 in 92 us, 6.3 TB/s.
 template <int SLOTS>
 __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constant__ ExCombineParams p) {
   const int lane = threadIdx.x & 31;
@@ -985,31 +991,29 @@ __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constan
     slot(t + gridDim.x, &next_row, &next_w);
     for (int c = threadIdx.x * 8; c - lane * 8 < hidden; c += blockDim.x * 8) {
       const int cr = min(c, static_cast<int>(p.yp) - 8);      // read column
-      const unsigned live = __ballot_sync(kFull, my_row >= 0);
       float2 v[4] = {};
-      for (int j0 = 0; j0 < p.top_k; j0 += SLOTS) {
+      for (int j0 = 0; j0 < p.top_k; j0 += SLOTS) {      // j0 + j < 32: top_k is at most 32
         uint4 y[SLOTS];
         uint32_t e[SLOTS];
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
-          const int64_t r = max(__shfl_sync(kFull, my_row, (j0 + j) & 31), 0);
-          y[j] = *reinterpret_cast<const uint4*>(p.y + r * p.yp + cr);
-          e[j] = p.yexp[r * p.yep + (cr >> 5)];
+          const int64_t r = __shfl_sync(kFull, my_row, j0 + j);
+          y[j] = make_uint4(0u, 0u, 0u, 0u);
+          e[j] = 0u;
+          if (r >= 0) {
+            y[j] = *reinterpret_cast<const uint4*>(p.y + r * p.yp + cr);
+            e[j] = p.yexp[r * p.yep + (cr >> 5)];
+          }
         }
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
-          const float wj = __shfl_sync(kFull, my_w, (j0 + j) & 31);
-          const bool on = j0 + j < 32 && ((live >> (j0 + j)) & 1u);
-          const float w = !on ? 0.f : wj * f(e[j] == 255u ? 0x7fffffffu : (e[j] - 13u) << 23);
-          const float2 w2 = make_float2(w, w), bias = make_float2(-8421376.f, -8421376.f);
-          const uint32_t u[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            // 2^23 + (value + 2^15) from its bits, less that, exactly
-            const float2 x = ptx::add2(make_float2(f(__byte_perm(u[q], 0x4b00u, 0x5410)),
-                                                   f(__byte_perm(u[q], 0x4b00u, 0x5432))), bias);
-            v[q] = ptx::fma2(w2, x, v[q]);
-          }
+          const float wj = __shfl_sync(kFull, my_w, j0 + j);
+          const float w = e[j] < kExpLeast ? 0.f : wj * f(e[j] == 255u ? 0x7fffffffu : (e[j] - 14u) << 23);
+          const float2 w2 = make_float2(w, w);
+          v[0] = ptx::fma2(w2, of_half(y[j].x), v[0]);
+          v[1] = ptx::fma2(w2, of_half(y[j].y), v[1]);
+          v[2] = ptx::fma2(w2, of_half(y[j].z), v[2]);
+          v[3] = ptx::fma2(w2, of_half(y[j].w), v[3]);
         }
       }
       const uint4 o = make_uint4(pack(v[0].x, v[0].y), pack(v[1].x, v[1].y), pack(v[2].x, v[2].y),
