@@ -503,7 +503,8 @@ muon_status_t muon_route_backward(const muon_route_config_t *cfg, const void *lo
  * the next product's operand).  A slot's product, a term of the sum over slots
  * (its weight comes after), is kept as 16-bit floats with one exponent per 32
  * columns, within 2^-11 of itself or 2^-39 of the largest magnitude of its 32
- * columns, or in fp32 for a few rows.  out bf16 [tokens, hidden], row stride out_stride.
+ * columns, or in fp32 for a few rows; an infinity or NaN stays in its column.
+ * out bf16 [tokens, hidden], row stride out_stride.
  * gu: bf16 [tokens * top_k, 2 * inner] or NULL: the gate and up values of
  * every row below offsets[experts], for muon_experts_backward (later rows
  * are not written).

@@ -400,14 +400,15 @@ __device__ __forceinline__ void epi_up(const ExGemmParams& p, const Tile& t, con
 
 // Rows for the sum over slots, as 16-bit floats (IEEE half) with one exponent
 // per row and 32 features (a warp's lanes): q = v * 2^(14 - e), e the exponent of
-// the piece's largest value.  A value keeps 11 bits while it is above 2^-28 of
+// the piece's largest finite value; infinities and NaN stay what and where they
+// are.  A value keeps 11 bits while it is above 2^-28 of
 // that largest one (below, its error is 2^-39 of it): a term errs by at most 2^-11
 // of itself, an eighth of what the bf16 operand behind it and the bf16 result
 // add, whatever its neighbours hold.  (15-bit integers, uniform in a piece, gave a
 // feature beside one 1000 times larger an error of 2.6 %; bf16 rows would add as
 // much as the result's rounding.)  Half of fp32's bytes are written and read
 // (16384 tokens over 256 x [768, 2048], product and sum: 398 + 167 us with fp32
-// rows, 378 + 91 with 16 bits).  A piece that holds an infinity or NaN is NaN.
+// rows, 378 + 91 with 16 bits).
 __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
   const int orow = w.tid >> 4, chunk = w.tid & 15, h = w.m0 + chunk * 8;
   __half* const y = p.y + static_cast<int64_t>(t.urow + orow) * p.yp + h;
@@ -422,20 +423,27 @@ __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, c
     // rows 8 i + 2 (lane % 4) (low half) and the next (high half): upper 16 bits
     // of the magnitudes, largest over this thread's 4 features, then the warp's 32
     uint32_t m[4];
+    auto largest = [&](bool only_finite) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = 0;
+      for (int i = 0; i < 4; ++i) {
+        m[i] = 0;
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          m[i] = __vmaxu2(m[i],
-                          __byte_perm(r[b][4 * i + 2 * q], r[b][4 * i + 2 * q + 1], 0x7632) & 0x7fff7fffu);
-    }
+          for (int q = 0; q < 2; ++q) {
+            uint32_t v = __byte_perm(r[b][4 * i + 2 * q], r[b][4 * i + 2 * q + 1], 0x7632) & 0x7fff7fffu;
+            if (only_finite) v &= ~__vcmpgeu2(v, 0x7f807f80u);
+            m[i] = __vmaxu2(m[i], v);
+          }
+      }
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1)
+      for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m[i] = __vmaxu2(m[i], __shfl_xor_sync(kFull, m[i], o));
+        for (int i = 0; i < 4; ++i) m[i] = __vmaxu2(m[i], __shfl_xor_sync(kFull, m[i], o));
+    };
+    largest(false);
+    if (__any_sync(kFull, __vmaxu2(__vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3])), 0x7f7f7f7fu) != 0x7f7f7f7fu))
+      largest(true);
     uint32_t e32 = 0;      // exponent of row c0 + lane, from a lane that holds its i and pair
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -446,8 +454,8 @@ __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, c
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 s;
-      s.x = f((268u - min(max((m[i] >> 7) & 0xffu, kExpLeast), 254u)) << 23);
-      s.y = f((268u - min(max(m[i] >> 23, kExpLeast), 254u)) << 23);
+      s.x = f((268u - max((m[i] >> 7) & 0xffu, kExpLeast)) << 23);
+      s.y = f((268u - max(m[i] >> 23, kExpLeast)) << 23);
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -965,9 +973,9 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
 }
 
 // out[t] = sum over slots, in slot order, a block per token, eight columns a
-// lane, SLOTS slots' loads in flight and the next token's rows with them (a slot
-// without a row loads nothing and counts as zeros); HBM-bound once the conversions
-// are few: 16384 tokens of 8 slots of 2048 in 92 us, 6.3 TB/s.
+// lane, SLOTS slots' loads in flight and the next token's rows with them;
+// HBM-bound once the conversions are few (no branch per slot: a slot without a row
+// reads row 0 and takes zeros): 16384 tokens of 8 slots of 2048 in 92 us, 6.3 TB/s.
 template <int SLOTS>
 __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constant__ ExCombineParams p) {
   const int lane = threadIdx.x & 31;
@@ -991,29 +999,28 @@ __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constan
     slot(t + gridDim.x, &next_row, &next_w);
     for (int c = threadIdx.x * 8; c - lane * 8 < hidden; c += blockDim.x * 8) {
       const int cr = min(c, static_cast<int>(p.yp) - 8);      // read column
+      const unsigned live = __ballot_sync(kFull, my_row >= 0);
       float2 v[4] = {};
       for (int j0 = 0; j0 < p.top_k; j0 += SLOTS) {      // j0 + j < 32: top_k is at most 32
         uint4 y[SLOTS];
         uint32_t e[SLOTS];
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
-          const int64_t r = __shfl_sync(kFull, my_row, j0 + j);
-          y[j] = make_uint4(0u, 0u, 0u, 0u);
-          e[j] = 0u;
-          if (r >= 0) {
-            y[j] = *reinterpret_cast<const uint4*>(p.y + r * p.yp + cr);
-            e[j] = p.yexp[r * p.yep + (cr >> 5)];
-          }
+          const int64_t r = max(__shfl_sync(kFull, my_row, j0 + j), 0);
+          y[j] = *reinterpret_cast<const uint4*>(p.y + r * p.yp + cr);
+          e[j] = p.yexp[r * p.yep + (cr >> 5)];
         }
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
           const float wj = __shfl_sync(kFull, my_w, j0 + j);
-          const float w = e[j] < kExpLeast ? 0.f : wj * f(e[j] == 255u ? 0x7fffffffu : (e[j] - 14u) << 23);
+          const bool on = (live >> (j0 + j)) & 1u;
+          const float w = on ? wj * f((e[j] - 14u) << 23) : 0.f;
           const float2 w2 = make_float2(w, w);
-          v[0] = ptx::fma2(w2, of_half(y[j].x), v[0]);
-          v[1] = ptx::fma2(w2, of_half(y[j].y), v[1]);
-          v[2] = ptx::fma2(w2, of_half(y[j].z), v[2]);
-          v[3] = ptx::fma2(w2, of_half(y[j].w), v[3]);
+          const uint32_t keep = on ? ~0u : 0u;      // what row 0 holds may be anything
+          v[0] = ptx::fma2(w2, of_half(y[j].x & keep), v[0]);
+          v[1] = ptx::fma2(w2, of_half(y[j].y & keep), v[1]);
+          v[2] = ptx::fma2(w2, of_half(y[j].z & keep), v[2]);
+          v[3] = ptx::fma2(w2, of_half(y[j].w & keep), v[3]);
         }
       }
       const uint4 o = make_uint4(pack(v[0].x, v[0].y), pack(v[1].x, v[1].y), pack(v[2].x, v[2].y),

@@ -1,5 +1,6 @@
 """The slot products' storage between the experts' products and the sum over
-slots (dx's terms likewise): features far larger than their neighbours.
+slots (dx's terms likewise): features far larger than their neighbours, and
+values that are not finite.
 
 Tolerances, per feature (a column of out or dx): the rounding of the product's
 operand to bf16 and of the result, each at most 2^-8 / sqrt(3) in root mean
@@ -64,3 +65,23 @@ def test_large_features_leave_their_neighbours_alone(ratio, hidden, inner):
         err, size = (got.double() - want).norm(dim=0), want.norm(dim=0)
         assert bool((err <= 3.5e-3 * size).all()), float((err / size).max())
     assert B.muon_query_status() == 0
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("tokens", [16, 17, 300])      # 32 rows go to the matrix-vector kernels
+def test_a_non_finite_feature_stays_alone(value, tokens):
+    x, dout, w_in, w_out, r = _case(tokens, 2, 96, 64, 4)
+    hit = (r.idx == 1).any(1)
+    out, gu = B.muon_experts_forward(x, w_in, w_out, r, save=True)
+    dx = B.muon_experts_backward(dout, x, w_in, w_out, r, gu, want_dw=False)[0]
+    bad_out, bad_in = w_out.clone(), w_in.clone()
+    bad_out[1, 37, 8] = value          # feature 37 of out, through expert 1
+    bad_in[1, 5, 70] = value           # feature 70 of dx, likewise
+    got = (B.muon_experts_forward(x, w_in, bad_out, r)[0],
+           B.muon_experts_backward(dout, x, bad_in, w_out, r, gu, want_dw=False)[0])
+    for a, want, col in zip(got, (out, dx), (37, 70)):
+        rest = [c for c in range(96) if c != col]
+        assert torch.equal(a[:, rest], want[:, rest])
+        assert torch.equal(a[~hit, col], want[~hit, col])
+        one = a[hit, col]
+        assert bool((one.isnan() if value != value else one.isinf()).all())
