@@ -500,10 +500,11 @@ muon_status_t muon_route_backward(const muon_route_config_t *cfg, const void *lo
  *   w_out  bf16 [experts, hidden, inner]
  *   weights, offsets, src, pos   as muon_route_forward wrote them
  * Products accumulate in fp32; the activation is rounded to bf16 once (it is
- * the next product's operand).  A slot's product, a term of the sum over slots
+ * the next product's operand on the tensor cores; at most 32 (token, slot)
+ * pairs are computed in fp32 throughout).  A slot's product, a term of the sum over slots
  * (its weight comes after), is kept as 16-bit floats with one exponent per 32
  * columns, within 2^-11 of itself or 2^-39 of the largest magnitude of its 32
- * columns, or in fp32 for a few rows; an infinity or NaN stays in its column.
+ * columns, or in fp32 for those few rows; an infinity or NaN stays in its column.
  * out bf16 [tokens, hidden], row stride out_stride.
  * gu: bf16 [tokens * top_k, 2 * inner] or NULL: the gate and up values of
  * every row below offsets[experts], for muon_experts_backward (later rows

@@ -233,7 +233,7 @@ struct ExFewParams {
   const int32_t* src;
   const int32_t* pos;
   __nv_bfloat16* gu;              // [rows][2 inner] or null
-  __nv_bfloat16* act;             // [rows][ip], 16-byte aligned rows
+  float* act;                     // [rows][ip], 16-byte aligned rows
   __nv_bfloat16* out;
   int64_t outs, tokens, ip;
   int hidden, inner, experts, top_k, rows;

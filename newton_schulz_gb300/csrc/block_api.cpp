@@ -568,7 +568,7 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
     // The tile kernels' latency (launches, a ring to fill, tiles for a part of
     // the SMs) against the weights' bytes per row.
     const int64_t ip = rup(I, 8);
-    const size_t at = cv.take(rows * ip * 2);
+    const size_t at = cv.take(rows * ip * 4);
     char* ws = nullptr;
     MUON_TRY(workspace(stream, cv.bytes, &ws));
     ExFewParams p;
@@ -576,7 +576,7 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
     p.x = static_cast<const __nv_bfloat16*>(a->x), p.xs = a->x_stride;
     p.w_in = static_cast<const __nv_bfloat16*>(a->w_in), p.w_out = static_cast<const __nv_bfloat16*>(a->w_out);
     p.weights = a->weights, p.offsets = a->offsets, p.src = a->src, p.pos = a->pos;
-    p.gu = static_cast<__nv_bfloat16*>(gu), p.act = reinterpret_cast<__nv_bfloat16*>(ws + at);
+    p.gu = static_cast<__nv_bfloat16*>(gu), p.act = reinterpret_cast<float*>(ws + at);
     p.out = static_cast<__nv_bfloat16*>(out), p.outs = outs;
     p.tokens = a->tokens, p.ip = ip, p.rows = static_cast<int>(rows);
     p.hidden = static_cast<int>(H), p.inner = static_cast<int>(I), p.experts = a->experts, p.top_k = a->top_k;

@@ -4,10 +4,11 @@
 // one column of out over all of a token's slots, 16 bytes a lane and load.
 // One token through 8 of 256 experts of [768, 2048] (75 MB): the tile kernels
 // took 34 us on 48 and 64 of their 76 CTA pairs' tiles, without the copy and
-// the sum over slots that they need besides; these two take 21.
-// The activation is rounded to bf16 as the tile kernels' operand is: in fp32
-// its reads, every warp's of the second kernel, took 2 us of that more (the
-// error of out against 64 bits 0.0017 instead of 0.0024 in norm).
+// the sum over slots that they need besides; these two take 23.
+// Everything is fp32 up to out: the activation is no tensor operand here, and
+// rounded to bf16 as the tile kernels must it would put out's error at 0.0024 in
+// norm instead of the result's own rounding, 0.0017 (and save 2 us of its reads,
+// every warp's of the second kernel).
 #include "block.h"
 #include "block_ptx.cuh"
 
@@ -53,6 +54,13 @@ __device__ __forceinline__ void dot8(const uint4& a, const uint4& b, float2& acc
   acc = ptx::fma2(two(a.y), two(b.y), acc);
   acc = ptx::fma2(two(a.z), two(b.z), acc);
   acc = ptx::fma2(two(a.w), two(b.w), acc);
+}
+// the same with fp32 a
+__device__ __forceinline__ void dot8(const float4& a0, const float4& a1, const uint4& b, float2& acc) {
+  acc = ptx::fma2(make_float2(a0.x, a0.y), two(b.x), acc);
+  acc = ptx::fma2(make_float2(a0.z, a0.w), two(b.y), acc);
+  acc = ptx::fma2(make_float2(a1.x, a1.y), two(b.z), acc);
+  acc = ptx::fma2(make_float2(a1.z, a1.w), two(b.w), acc);
 }
 // weights are read once
 __device__ __forceinline__ uint4 ld_once(const __nv_bfloat16* p) {
@@ -107,7 +115,7 @@ __global__ void __launch_bounds__(kWarps * 32) ex_few_up_kernel(const __grid_con
   }
   const float gate = warp_sum(ag.x + ag.y), up = warp_sum(au.x + au.y);
   if (lane == 0) {
-    p.act[row * p.ip + ft] = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
+    p.act[row * p.ip + ft] = gate / (1.f + __expf(-gate)) * up;
     if (p.gu) {
       __nv_bfloat16* o = p.gu + static_cast<int64_t>(row) * 2 * p.inner + ft;
       o[0] = __float2bfloat16_rn(gate);
@@ -141,7 +149,8 @@ __global__ void __launch_bounds__(kWarps * 32) ex_few_down_kernel(const __grid_c
   float acc = 0.f;
   constexpr int kSlots = 4;
   for (int j0 = 0; j0 < p.top_k; j0 += kSlots) {
-    const __nv_bfloat16 *w[kSlots], *a[kSlots];
+    const __nv_bfloat16* w[kSlots];
+    const float* a[kSlots];
     float wt[kSlots];
 #pragma unroll
     for (int j = 0; j < kSlots; ++j) {
@@ -156,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32) ex_few_down_kernel(const __grid_c
     float2 d[kSlots] = {};
     if (p.vec_out) {
       for (int c = lane * 8; c < p.inner; c += 512) {
-        uint4 wv[kSlots][2], av[kSlots][2];
+        uint4 wv[kSlots][2];
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
 #pragma unroll
@@ -164,15 +173,19 @@ __global__ void __launch_bounds__(kWarps * 32) ex_few_down_kernel(const __grid_c
             if (w[j] && c + 256 * q < p.inner) wv[j][q] = ld_once(w[j] + c + 256 * q);
         ptx::wait_dependency();      // act; the first weights are on their way meanwhile
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j)
+        for (int q = 0; q < 2; ++q) {
+          float4 av[kSlots][2];
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            if (w[j] && c + 256 * q < p.inner) av[j][q] = ld(a[j] + c + 256 * q);
+          for (int j = 0; j < kSlots; ++j)
+            if (w[j] && c + 256 * q < p.inner) {
+              const float4* from = reinterpret_cast<const float4*>(a[j] + c + 256 * q);
+              av[j][0] = from[0];
+              av[j][1] = from[1];
+            }
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j)
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            if (w[j] && c + 256 * q < p.inner) dot8(av[j][q], wv[j][q], d[j]);
+          for (int j = 0; j < kSlots; ++j)
+            if (w[j] && c + 256 * q < p.inner) dot8(av[j][0], av[j][1], wv[j][q], d[j]);
+        }
       }
     } else {
       ptx::wait_dependency();
@@ -180,7 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32) ex_few_down_kernel(const __grid_c
       for (int j = 0; j < kSlots; ++j)
         if (w[j])
           for (int c = lane; c < p.inner; c += 32)
-            d[j].x = fmaf(__bfloat162float(a[j][c]), __bfloat162float(w[j][c]), d[j].x);
+            d[j].x = fmaf(a[j][c], __bfloat162float(w[j][c]), d[j].x);
     }
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
