@@ -148,8 +148,13 @@ __device__ __forceinline__ float softmax_parts(const float (&x)[EPL], float (&e)
   return warp_sum(sum);
 }
 
-// the quotient within 2 units of the last place
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+// 1 / (1 + exp(-x)) within 3 units of the last place: from exp(-|x|), so that the
+// approximate quotient's divisor is in [1, 2] (past 2^126, the scores of logits
+// below -87.3, it gives 0).
+__device__ __forceinline__ float sigmoid(float x) {
+  const float t = expf(-fabsf(x)), r = __fdividef(1.f, 1.f + t);
+  return x < 0.f ? t * r : r;
+}
 
 }  // namespace
 
