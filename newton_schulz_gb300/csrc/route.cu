@@ -148,12 +148,19 @@ __device__ __forceinline__ float softmax_parts(const float (&x)[EPL], float (&e)
   return warp_sum(sum);
 }
 
-// 1 / (1 + exp(-x)) within 3 units of the last place: from exp(-|x|), so that the
-// approximate quotient's divisor is in [1, 2] (past 2^126, the scores of logits
-// below -87.3, it gives 0).
+// s = 1 / (1 + exp(-x)) and rest = 1 - s.  From exp(-|x|), so the approximate
+// quotient's divisor is in [1, 2] (it gives 0 past 2^126, the scores of logits
+// below -87.3), and neither s of a low logit nor rest of a high one is the
+// difference of numbers near 1 (from logit 17 on that would be 0): each within
+// 3 units of the last place.
+__device__ __forceinline__ float sigmoid(float x, float* rest) {
+  const float t = expf(-fabsf(x)), r = __fdividef(1.f, 1.f + t), q = t * r;
+  *rest = x < 0.f ? r : q;
+  return x < 0.f ? q : r;
+}
 __device__ __forceinline__ float sigmoid(float x) {
-  const float t = expf(-fabsf(x)), r = __fdividef(1.f, 1.f + t);
-  return x < 0.f ? t * r : r;
+  float rest;
+  return sigmoid(x, &rest);
 }
 
 }  // namespace
@@ -330,6 +337,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   float x[EPL], sc[EPL], d[EPL];
   load_logits<EPL>(x, p.logits, p.dtype, tok * p.stride, p.experts, p.vec, lane);
   only_finite<EPL>(x);
+  float rest[EPL];       // sigmoid: 1 - score
   if (p.score == 0) {
     float top;
     const float sum = softmax_parts<EPL>(x, sc, &top);
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     for (int i = 0; i < EPL; ++i) sc[i] *= inv;
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) sc[i] = sigmoid(x[i]);
+    for (int i = 0; i < EPL; ++i) sc[i] = sigmoid(x[i], &rest[i]);
   }
   int32_t e = -1;
   float dw = 0.f;
@@ -389,7 +397,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   for (int i = 0; i < EPL; ++i)
     // renormalised softmax: sum over the chosen of d q is zero, so the full
     // softmax's slope is q d as well
-    d[i] = p.score == 0 ? sc[i] * (d[i] - sub) : d[i] * sc[i] * (1.f - sc[i]);
+    d[i] = p.score == 0 ? sc[i] * (d[i] - sub) : d[i] * sc[i] * rest[i];
   const int first = lane * EPL;
   const int64_t at = tok * p.dstride + first;
   if (p.dtype == kDtF32) store_share<EPL>(static_cast<float*>(p.dlogits) + at, d, p.experts - first, p.dvec);

@@ -1,4 +1,4 @@
-"""Routing scores where an exponential is large or small.
+"""Routing scores and their gradients where an exponential is large or small.
 
 Tolerances: an exponential (2 units of the last place), a quotient (2) and at
 most three products (half a unit each) are under 8 * 2^-24 = 5e-7 of the
@@ -22,6 +22,20 @@ def _dev(lib, cuda_ok):
 
 def _np(t):
     return t.detach().double().cpu().numpy()
+
+
+def test_sigmoid_gradient_of_large_logits():
+    # s (1 - s): 1 - s is 4e-8 at 17 and below half a unit of s's last place there
+    x = torch.tensor([[a, -a, b, -b] for a in (8.0, 10.0, 12.0, 14.5) for b in (16.0, 17.5, 20.0, 40.0, 80.0)],
+                     device="cuda")
+    cfg = B.make_route_config(4, 4, score=B.ROUTE_SIGMOID)
+    r = B.muon_route_forward(x, cfg)
+    dw = torch.randn(x.shape[0], 4, generator=torch.Generator().manual_seed(1)).cuda()
+    got = _np(B.muon_route_backward(x, cfg, r.idx, dw))
+    l, d = _np(x), np.zeros(x.shape)
+    np.put_along_axis(d, r.idx.cpu().numpy().astype(np.int64), _np(dw), 1)
+    want = d / (1 + np.exp(-l)) / (1 + np.exp(l))
+    assert np.all(np.abs(got - want) <= 2e-6 * np.abs(want) + 2.0 ** -149)
 
 
 def test_sigmoid_weights_of_very_low_logits():
