@@ -373,31 +373,35 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 #pragma unroll
   for (int i = 0; i < EPL; ++i) d[i] = mine[i];
   if (p.renorm) {
+    // q_i, the chosen scores over their sum; then q_i (d_i - sum d q), where the
+    // sum over the chosen is zero, so the full softmax's slope is that as well.
+    // The scores are divided, not d: their sum may be as small as 2^-149.
     float total = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const float q = (chosen >> i) & 1u ? sc[i] : 0.f;
-      total += q;
-      dot = fmaf(d[i], q, dot);
+      sc[i] = (chosen >> i) & 1u ? sc[i] : 0.f;
+      total += sc[i];
     }
     total = warp_sum(total);
-    dot = warp_sum(dot);
-    const float mean = total > 0.f ? dot / total : 0.f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      d[i] = ((chosen >> i) & 1u) && total > 0.f ? (d[i] - mean) / total : 0.f;
-  }
-  float sub = 0.f;
-  if (p.score == 0 && !p.renorm) {
+    for (int i = 0; i < EPL; ++i) {
+      sc[i] = total > 0.f ? sc[i] / total : 0.f;
+      dot = fmaf(d[i], sc[i], dot);
+    }
+    dot = warp_sum(dot);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) d[i] = sc[i] * (d[i] - dot) * (p.score == 0 ? 1.f : rest[i]);
+  } else if (p.score == 0) {
+    float sub = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sub = fmaf(d[i], sc[i], sub);
     sub = warp_sum(sub);
-  }
 #pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    // renormalised softmax: sum over the chosen of d q is zero, so the full
-    // softmax's slope is q d as well
-    d[i] = p.score == 0 ? sc[i] * (d[i] - sub) : d[i] * sc[i] * rest[i];
+    for (int i = 0; i < EPL; ++i) d[i] = sc[i] * (d[i] - sub);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) d[i] *= sc[i] * rest[i];
+  }
   const int first = lane * EPL;
   const int64_t at = tok * p.dstride + first;
   if (p.dtype == kDtF32) store_share<EPL>(static_cast<float*>(p.dlogits) + at, d, p.experts - first, p.dvec);

@@ -50,3 +50,25 @@ def test_sigmoid_weights_of_very_low_logits():
     plain = B.muon_route_forward(x, B.make_route_config(4, 3, score=B.ROUTE_SIGMOID)).weights
     s = np.take_along_axis(1 / (1 + np.exp(-_np(x))), idx, 1)
     assert np.all(np.abs(_np(plain) - s) <= 2e-6 * s + 2.0 ** -148)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_renormalised_gradient_of_small_scores(score):
+    # a bias sends a token to experts whose scores are tiny; the gradient is of
+    # the weights' size times 1 - s, whatever the scores' sum
+    x = torch.tensor([[0.0, -85.0, -86.0, -86.5], [0.0, -86.9, -84.0, -85.5]], device="cuda")
+    bias = torch.tensor([-2.0, 1.0, 1.5, 2.0], device="cuda")
+    cfg = B.make_route_config(4, 3, score=getattr(B, "ROUTE_" + score.upper()), renormalize=True, scale=2.5)
+    r = B.muon_route_forward(x, cfg, bias=bias)
+    assert r.idx.tolist() == [[3, 2, 1]] * 2
+    dw = torch.tensor([[120.0, -80.0, 55.0], [-90.0, 70.0, 100.0]], device="cuda")
+    got = _np(B.muon_route_backward(x, cfg, r.idx, dw))
+    l, w = _np(x), _np(dw)
+    want = np.zeros_like(l)
+    for t in range(2):
+        at = r.idx[t].tolist()
+        q = np.exp(l[t, at])
+        q /= q.sum()
+        want[t, at] = 2.5 * q * (w[t] - (w[t] * q).sum())
+    # (the sigmoid's 1 - s and the softmax's rest are 1 to 64 bits here)
+    assert np.all(np.abs(got - want) <= 4e-6 * 2.5 * np.abs(w).max(1, keepdims=True))
