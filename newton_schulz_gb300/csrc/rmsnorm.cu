@@ -198,6 +198,11 @@ __device__ __forceinline__ void row_reduce2(float& a, float& b, int tpr, float* 
   }
 }
 
+// What e4m3 values are multiplied by for their codes.  The approximate quotient
+// gives 0 for divisors past 2^126; a scale, the largest magnitude over 448, stays
+// below that, the magnitude itself does not.
+__device__ __forceinline__ float code_factor(float scale) { return __fdividef(1.f, scale); }
+
 }  // namespace
 
 // One row from its loaded chunks: statistics, h, y.
@@ -281,17 +286,17 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const Chunk<WIDE> 
     for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = fmaxf(m, 1e-12f);
     if (live && col < p.cols) {
-      const float k = __fdividef(448.f, m);
+      const float scale = m * (1.f / 448.f), k = code_factor(scale);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= k;
       store_chunk(yr, kDtE4m3, col, p.cols, vec, v);
-      if ((c & 15) == 0) p.scales[row * p.n_scales + (c >> 4)] = m * (1.f / 448.f);
+      if ((c & 15) == 0) p.scales[row * p.n_scales + (c >> 4)] = scale;
     }
   }
   if (!e4m3 || p.grouped) return;
   // one scale for the row
   top = fmaxf(row_reduce<true>(top, tpr, s_max), 1e-12f);
-  const float k = __fdividef(448.f, top);
+  const float scale = top * (1.f / 448.f), k = code_factor(scale);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int col = (i * tpr + t) * 8;
@@ -301,7 +306,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const Chunk<WIDE> 
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= k;
     store_chunk(yr, kDtE4m3, col, p.cols, vec, v);
-    if (col == 0) p.scales[row] = top * (1.f / 448.f);
+    if (col == 0) p.scales[row] = scale;
   }
 }
 
