@@ -486,6 +486,16 @@ def _rows(t, name: str, cols: Optional[int] = None, rows: Optional[int] = None):
     return t.data_ptr(), stride, _code(t.dtype)
 
 
+def _as_current(stream):
+    """Context in which `stream` (a torch stream or a raw handle) is the current
+    one.  The block's calls allocate their outputs in it: memory of another
+    stream may still be written by work that was enqueued there before the call."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _like(t, dtype=None):
     """An uninitialised contiguous tensor of t's shape (torch.empty_like is the
     cheapest allocation from Python; it would keep a view's strides)."""
@@ -513,6 +523,9 @@ def muon_rmsnorm_forward(x, gain=None, residual=None, eps: float = 1e-6, y_dtype
     is None without a residual unless given.  Outputs that are not given are
     allocated; h may be `residual` itself."""
     import torch
+    if stream is not None:
+        with _as_current(stream):
+            return muon_rmsnorm_forward(x, gain, residual, eps, y_dtype, group, h, y, scales)
     xp, xs, xc = _rows(x, "x")
     rows, cols = x.shape
     rp, rs, rc, gp, gc, hp, hs, hc, sp = None, 0, 0, None, 0, None, 0, 0, None
@@ -537,7 +550,7 @@ def muon_rmsnorm_forward(x, gain=None, residual=None, eps: float = 1e-6, y_dtype
     else:
         scales = None
     a = RmsNorm(rows, cols, xp, xs, rp, rs, gp, hp, hs, yp, ys, sp, xc, rc, gc, hc, yc, group, eps)
-    check(load().muon_rmsnorm_forward(a, _stream_ptr(stream)), "muon_rmsnorm_forward")
+    check(load().muon_rmsnorm_forward(a, _stream_ptr(None)), "muon_rmsnorm_forward")
     return y, h, scales
 
 
@@ -548,6 +561,9 @@ def muon_rmsnorm_backward(dy, h, gain=None, dres=None, eps: float = 1e-6, dh=Non
     h along the residual stream, added; dgain is f32 [cols] (None when not
     wanted)."""
     import torch
+    if stream is not None:
+        with _as_current(stream):
+            return muon_rmsnorm_backward(dy, h, gain, dres, eps, dh, dgain, want_dgain)
     dp, ds, dc = _rows(dy, "dy")
     rows, cols = dy.shape
     hp, hs, hc = _rows(h, "h", cols, rows)
@@ -564,7 +580,7 @@ def muon_rmsnorm_backward(dy, h, gain=None, dres=None, eps: float = 1e-6, dh=Non
     if dgain is not None:
         wp = _dense(dgain, "dgain", (cols,), torch.float32)
     a = RmsNormGrad(rows, cols, dp, ds, hp, hs, gp, rp, rs, op, os_, wp, dc, hc, gc, rc, oc, eps)
-    check(load().muon_rmsnorm_backward(a, _stream_ptr(stream)), "muon_rmsnorm_backward")
+    check(load().muon_rmsnorm_backward(a, _stream_ptr(None)), "muon_rmsnorm_backward")
     return dh, dgain
 
 
@@ -590,6 +606,9 @@ def muon_route_forward(logits, cfg: RouteConfig, bias=None, mask=None, plan: boo
     bias: f32 [experts], seen by the choice only.  mask: bool or uint8
     [tokens], tokens to leave out are false."""
     import torch
+    if stream is not None:
+        with _as_current(stream):
+            return muon_route_forward(logits, cfg, bias, mask, plan)
     ptr, stride, code = _rows(logits, "logits", cfg.experts)
     tokens, k, dev = logits.shape[0], cfg.top_k, logits.device
     idx = torch.empty((tokens, k), dtype=torch.int32, device=dev)
@@ -603,7 +622,7 @@ def muon_route_forward(logits, cfg: RouteConfig, bias=None, mask=None, plan: boo
     if mask is not None:
         m = _dense(mask, "mask", (tokens,), torch.bool if mask.dtype == torch.bool else torch.uint8)
     check(load().muon_route_forward(cfg, ptr, code, stride, tokens, b, m, idx.data_ptr(),
-                                    weights.data_ptr(), op, sp, pp, _stream_ptr(stream)),
+                                    weights.data_ptr(), op, sp, pp, _stream_ptr(None)),
           "muon_route_forward")
     return Route(idx, weights, off, src, pos)
 
@@ -611,17 +630,23 @@ def muon_route_forward(logits, cfg: RouteConfig, bias=None, mask=None, plan: boo
 def muon_route_plan(idx, experts: int, stream=None):
     """(offsets, src, pos) of int32 CUDA idx [tokens, top_k]: the pairs' rows in expert order."""
     import torch
+    if stream is not None:
+        with _as_current(stream):
+            return muon_route_plan(idx, experts)
     tokens, top_k = idx.shape
     p = _dense(idx, "idx", (tokens, top_k), torch.int32)
     off, src, pos = _plan_tensors(idx.device, tokens, top_k, experts)
     check(load().muon_route_plan(p, tokens, top_k, experts, off.data_ptr(), src.data_ptr(),
-                                 pos.data_ptr(), _stream_ptr(stream)), "muon_route_plan")
+                                 pos.data_ptr(), _stream_ptr(None)), "muon_route_plan")
     return off, src, pos
 
 
 def muon_route_backward(logits, cfg: RouteConfig, idx, dweights, dlogits=None, stream=None):
     """Gradient of the routing weights with respect to the logits (their dtype)."""
     import torch
+    if stream is not None:
+        with _as_current(stream):
+            return muon_route_backward(logits, cfg, idx, dweights, dlogits)
     ptr, stride, code = _rows(logits, "logits", cfg.experts)
     tokens = logits.shape[0]
     if dlogits is None:
@@ -632,7 +657,7 @@ def muon_route_backward(logits, cfg: RouteConfig, idx, dweights, dlogits=None, s
     i = _dense(idx, "idx", (tokens, cfg.top_k), torch.int32)
     w = _dense(dweights, "dweights", (tokens, cfg.top_k), torch.float32)
     check(load().muon_route_backward(cfg, ptr, code, stride, tokens, i, w, dptr, dstride,
-                                     _stream_ptr(stream)), "muon_route_backward")
+                                     _stream_ptr(None)), "muon_route_backward")
     return dlogits
 
 
@@ -664,6 +689,9 @@ def muon_experts_forward(x, w_in, w_out, route: Route, save: bool = False, out=N
     rows, then up rows), w_out [experts, hidden, inner].  gu, what
     muon_experts_backward needs, is None unless `save`."""
     import torch
+    if stream is not None:
+        with _as_current(stream):
+            return muon_experts_forward(x, w_in, w_out, route, save, out)
     a = _experts_args(x, w_in, w_out, route)
     if out is None:
         out = _like(x)
@@ -674,7 +702,7 @@ def muon_experts_forward(x, w_in, w_out, route: Route, save: bool = False, out=N
     if save:
         gu = torch.empty((a.tokens * a.top_k, 2 * a.inner), dtype=torch.bfloat16, device=x.device)
     check(load().muon_experts_forward(a, optr, ostride,
-                                      gu.data_ptr() if save else None, _stream_ptr(stream)),
+                                      gu.data_ptr() if save else None, _stream_ptr(None)),
           "muon_experts_forward")
     return out, gu
 
@@ -686,6 +714,10 @@ def muon_experts_backward(dout, x, w_in, w_out, route: Route, gu, dw_dtype=None,
     shapes, as muon_step_grouped takes them; dweights is f32 [tokens, top_k]
     for muon_route_backward."""
     import torch
+    if stream is not None:
+        with _as_current(stream):
+            return muon_experts_backward(dout, x, w_in, w_out, route, gu, dw_dtype, dx, dw_in, dw_out, want_dx,
+                                         want_dw)
     a = _experts_args(x, w_in, w_out, route)
     bf16 = torch.bfloat16
     if dout.dtype != bf16 or (dx is not None and dx.dtype != bf16):
@@ -709,5 +741,5 @@ def muon_experts_backward(dout, x, w_in, w_out, route: Route, gu, dw_dtype=None,
         a, dptr, dstride, g, xptr, xstride,
         _dense(dw_in, "dw_in", w_in.shape, dw_dtype) if want_dw else None,
         _dense(dw_out, "dw_out", w_out.shape, dw_dtype) if want_dw else None,
-        code, dweights.data_ptr(), _stream_ptr(stream)), "muon_experts_backward")
+        code, dweights.data_ptr(), _stream_ptr(None)), "muon_experts_backward")
     return dx, dw_in, dw_out, dweights
