@@ -362,8 +362,9 @@ muon_status_t muon_debug_guard_check(cudaStream_t stream, int64_t *bad_bytes);
  * Conventions, besides those at the top of this file:
  *   - Row strides are in elements and at least the row's width; a stride is
  *     read only where there is more than one row.
- *   - Outputs must not overlap inputs or each other (MUON_ERR_ALIAS) except
- *     where an entry point allows it.
+ *   - Outputs must not share elements with inputs or each other (MUON_ERR_ALIAS)
+ *     except where an entry point allows it.  Columns of one buffer's rows may
+ *     be used side by side; views of different pitches must not interleave.
  *   - 16-byte aligned pointers and strides of a multiple of 16 bytes are
  *     fastest; any element-aligned pointer and any stride works.
  * ====================================================================== */

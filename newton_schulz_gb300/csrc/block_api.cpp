@@ -26,7 +26,16 @@ struct View {
   uintptr_t hi() const {
     return rows <= 0 ? lo() : lo() + static_cast<uintptr_t>(((rows - 1) * stride + cols) * esize(dt));
   }
-  bool overlaps(const View& o) const { return p && o.p && lo() < o.hi() && o.lo() < hi(); }
+  // Whether an element is in both: their spans meet, and they are not different
+  // columns of rows one pitch apart (or one row between such rows' columns).
+  bool overlaps(const View& o) const {
+    if (!p || !o.p || lo() >= o.hi() || o.lo() >= hi()) return false;
+    const int64_t pa = stride * esize(dt), pb = o.stride * esize(o.dt);
+    if ((rows <= 1 && o.rows <= 1) || (rows > 1 && o.rows > 1 && pa != pb)) return true;
+    const int64_t pitch = rows > 1 ? pa : pb, wa = cols * esize(dt), wb = o.cols * esize(o.dt);
+    const int64_t d = static_cast<int64_t>(o.lo() - lo()) % pitch, at = d < 0 ? d + pitch : d;
+    return at < wa || at + wb > pitch;
+  }
   bool same(const View& o) const { return p == o.p && dt == o.dt && (stride == o.stride || rows <= 1); }
   bool bad_stride() const { return rows > 1 && (stride < cols || stride > (int64_t(1) << 40)); }
   // every row starts on a 16-byte boundary
