@@ -85,6 +85,7 @@ struct NormGradParams {
   float eps, inv_cols;
   unsigned* status;
   unsigned long long timeout_ns;
+  int inject;                         // testing hook (set at the launch): row 0 never arrives
 };
 
 cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t s);

@@ -339,9 +339,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 8 ? 512 : 256, NV == 2 
   norm_row<NV, WIDE>(p, cx, cr, row, live, t, tpr, s_sum, s_max);
 }
 
-// Bounded wait of a whole block on one of its ring's stages; false: gave up.
-__device__ __forceinline__ bool ring_wait(uint64_t* full, uint32_t parity, unsigned* status,
-                                          unsigned long long timeout_ns) {
+__device__ __forceinline__ bool wait_bounded(uint64_t* full, uint32_t parity, unsigned* status,
+                                             unsigned long long timeout_ns) {
   const uint32_t bar = ptx::smem_u32(full);
   bool ok = ptx::mbar_try_wait(bar, parity);
   if (!ok) {
@@ -352,7 +351,12 @@ __device__ __forceinline__ bool ring_wait(uint64_t* full, uint32_t parity, unsig
         break;
       }
   }
-  return !__syncthreads_or(!ok);
+  return ok;
+}
+// Of a whole block on one of its ring's stages; false: gave up.
+__device__ __forceinline__ bool ring_wait(uint64_t* full, uint32_t parity, unsigned* status,
+                                          unsigned long long timeout_ns) {
+  return !__syncthreads_or(!wait_bounded(full, parity, status, timeout_ns));
 }
 
 // Gradient: row slot s takes rows s, s + slots, ...; its share of dgain stays
@@ -468,6 +472,7 @@ __global__ void __launch_bounds__(256, 2)
   auto fetch = [&](int64_t row, int s) {
     uint8_t* d = ring + s * pitch;
     ptx::mbar_arrive_expect_tx(&full[s], bytes);
+    if (p.inject && row == 0) return;      // testing hook: the wait for row 0 runs out
     ptx::bulk_load(d, row_ptr(p.dy, p.dy_dt, row, p.dys), bd, &full[s]);
     ptx::bulk_load(d + bd, row_ptr(p.h, p.h_dt, row, p.hs), bh, &full[s]);
     if (has_res) ptx::bulk_load(d + bd + bh, row_ptr(p.dres, p.dr_dt, row, p.drs), bs, &full[s]);
@@ -493,7 +498,8 @@ __global__ void __launch_bounds__(256, 2)
   }
   int s = 0, par = 0;
   uint32_t phase = 0;
-  for (int64_t row = blockIdx.x; row < rows; row += step) {
+  int64_t row = blockIdx.x;
+  for (; row < rows; row += step) {
     if (!ring_wait(&full[s], phase, p.status, p.timeout_ns)) break;
     const uint8_t* d = ring + s * pitch;
     Chunk<WIDE> cd[NV], ch[NV], cs[NV];
@@ -549,6 +555,12 @@ __global__ void __launch_bounds__(256, 2)
       store_chunk(out, p.dh_dt, col, p.cols, true, v);
     }
   }
+  // gave up: the copies still on their way end before the block's memory does
+  if (t == 0)
+    for (int k = 0; k < stages && row + static_cast<int64_t>(k) * step < rows; ++k) {
+      const int at = s + k < stages ? s + k : s + k - stages;
+      wait_bounded(&full[at], phase ^ (s + k < stages ? 0u : 1u), p.status, p.timeout_ns);
+    }
   if (p.part) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -661,10 +673,11 @@ GradShape grad_shape(const NormGradParams& p, int sms) {
 }
 
 template <int NV, bool WIDE>
-cudaError_t ring_launch(const NormGradParams& p, const GradShape& g, cudaStream_t s) {
+cudaError_t ring_launch(NormGradParams p, const GradShape& g, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(rmsnorm_grad_ring_kernel<NV, WIDE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytes);
   if (e != cudaSuccess) return e;
+  p.inject = take_injected_stall(kInjectGemm);
   rmsnorm_grad_ring_kernel<NV, WIDE><<<g.grid, g.block, g.smem, s>>>(p, g.stages);
   return cudaGetLastError();
 }
