@@ -879,14 +879,14 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThread
       }
       if (t.kb > 0) {
         // One thread of the set waits and decides for all (they share a barrier,
-        // which costs nothing while it holds them); the slot alternates, so it is
-        // rewritten only after everyone has read it.
+        // which costs nothing while it holds them); the slot alternates with the
+        // accumulator, so the next tile that waits has its barrier between two uses.
         if (w.tid == 0) {
           wait_bounded(&tfull[buf], (acc >> 1) & 1, abort_flag, p.status, p.timeout_ns, false);
-          s_ok[2 * w.set + (it & 1)] = !*abort_flag;
+          s_ok[2 * w.set + buf] = !*abort_flag;
         }
         w.bar();
-        if (!s_ok[2 * w.set + (it & 1)]) break;
+        if (!s_ok[2 * w.set + buf]) break;
         ptx::tc_fence_after();
       }
       if (KIND == kExUp) epi_up(p, t, w);
