@@ -750,6 +750,10 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThread
           break;
         }
         if (crank == 0) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
+        if (p.inject && blockIdx.x == 0 && issued == 0) {      // testing hook: nothing comes for it
+          issued = stage = 1;
+          continue;
+        }
         const uint32_t bar = full0 + stage * 8;
         uint8_t* a = sStage + stage * kStageBytes;
         uint8_t* b = a + kOpBytes;
@@ -1079,6 +1083,7 @@ int resident_ctas(int sms, int smem) {
 
 template <int KIND, int PAIRS>
 cudaError_t gemm_launch(ExGemmParams p, int sms, bool early, cudaStream_t s) {
+  p.inject = take_injected_stall(kInjectGemm);
   p.stages = kMostStages;
   if (gemm_smem(KIND, p.stages, p.experts) > kSmemLimit) p.stages = kMostStages - 1;
   const int smem = gemm_smem(KIND, p.stages, p.experts);

@@ -46,3 +46,19 @@ def _stall(call, monkeypatch):
 def test_norm_gradient_ring(cols, dtype, monkeypatch):
     dy, h, gain = _randn(3000, cols, dtype=dtype), _randn(3000, cols, dtype=dtype, seed=2), _randn(cols, seed=3)
     _stall(lambda: B.muon_rmsnorm_backward(dy, h, gain, dres=dy), monkeypatch)
+
+
+# hidden and inner that take one pair, and clusters of two
+@pytest.mark.parametrize("tokens,hidden,inner", [(300, 256, 136), (1500, 1024, 1024)])
+@pytest.mark.parametrize("back", [False, True])
+def test_experts_products(tokens, hidden, inner, back, monkeypatch):
+    idx = torch.stack([torch.arange(tokens) % 3, torch.full((tokens,), 4)], 1).to(torch.int32).cuda()
+    r = B.Route(idx, _randn(tokens, 2, dtype=F32).abs(), *B.muon_route_plan(idx, 5))      # expert 3 has no rows
+    x, dout = _randn(tokens, hidden), _randn(tokens, hidden, seed=2)
+    w_in = _randn(5, 2 * inner, hidden, seed=3) * hidden ** -0.5
+    w_out = _randn(5, hidden, inner, seed=4) * inner ** -0.5
+    if not back:
+        _stall(lambda: B.muon_experts_forward(x, w_in, w_out, r)[:1], monkeypatch)
+        return
+    gu = B.muon_experts_forward(x, w_in, w_out, r, save=True)[1]
+    _stall(lambda: B.muon_experts_backward(dout, x, w_in, w_out, r, gu), monkeypatch)
