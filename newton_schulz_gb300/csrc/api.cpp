@@ -1536,6 +1536,21 @@ int api_workspace(cudaStream_t stream, size_t bytes, char** out) {
   return get_workspace(stream, bytes, 1, out, &ctr);
 }
 
+size_t api_guard_bytes() { return env_size("MUON_WS_GUARD", 0) ? kGuardBytes : 0; }
+
+int api_guard_fill(char* ws, const std::vector<size_t>& bands, cudaStream_t stream) {
+  DevState* d = nullptr;
+  muon_status_t st = dev_state(&d);
+  if (st == MUON_OK) st = guard_counter(d);
+  return st == MUON_OK ? guard_fill(ws, bands, kGuardBytes, stream) : st;
+}
+
+int api_guard_check(char* ws, const std::vector<size_t>& bands, cudaStream_t stream) {
+  DevState* d = nullptr;
+  const muon_status_t st = dev_state(&d);
+  return st == MUON_OK ? guard_check(ws, bands, kGuardBytes, d, stream) : st;
+}
+
 void api_set_launches(int n) { t_last_launches = n; }
 }  // namespace muon
 

@@ -9,6 +9,7 @@
 
 #include <mutex>
 #include <type_traits>
+#include <vector>
 
 #include "muon_internal.h"
 
@@ -20,12 +21,17 @@ struct ApiDevice {
   unsigned* status;                  // device status word
   unsigned long long timeout_ns;     // bound of a device wait
 };
-// Both are called with api_mutex() held.  api_workspace: at least `bytes`
+// All are called with api_mutex() held.  api_workspace: at least `bytes`
 // bytes of the (device, stream) workspace, whose contents last until the next
-// call on that stream.
+// call on that stream.  api_guard_bytes: size of the band behind every buffer in
+// guard mode (MUON_WS_GUARD), else 0; bands are filled before the call's launches
+// and checked after them.
 std::mutex& api_mutex();
 int api_device(ApiDevice* out);                                          // muon_status_t
 int api_workspace(cudaStream_t stream, size_t bytes, char** out);        // muon_status_t
+size_t api_guard_bytes();
+int api_guard_fill(char* ws, const std::vector<size_t>& bands, cudaStream_t stream);    // muon_status_t
+int api_guard_check(char* ws, const std::vector<size_t>& bands, cudaStream_t stream);   // muon_status_t
 void api_set_launches(int n);
 
 // Launch of a kernel that follows another of the same call.  early: it may

@@ -60,9 +60,31 @@ struct Counter {
   } while (0)
 
 muon_status_t device(ApiDevice* d) { return static_cast<muon_status_t>(api_device(d)); }
-muon_status_t workspace(cudaStream_t s, size_t n, char** out) {
-  return static_cast<muon_status_t>(api_workspace(s, n, out));
-}
+
+// Workspace, cut into 256-byte aligned pieces, each followed by a guard band in
+// guard mode: sizes first, then pointers, then the launches between open and close.
+struct Carve {
+  size_t bytes = 0;
+  const size_t guard = api_guard_bytes();
+  std::vector<size_t> bands;
+  char* ws = nullptr;
+  size_t take(int64_t n) {
+    const size_t at = bytes;
+    bytes += pad256(static_cast<size_t>(n));
+    if (guard) {
+      bands.push_back(bytes);
+      bytes += guard;
+    }
+    return at;
+  }
+  muon_status_t open(cudaStream_t s) {
+    const muon_status_t st = static_cast<muon_status_t>(api_workspace(s, bytes, &ws));
+    return st != MUON_OK || !guard ? st : static_cast<muon_status_t>(api_guard_fill(ws, bands, s));
+  }
+  muon_status_t close(cudaStream_t s) {
+    return guard ? static_cast<muon_status_t>(api_guard_check(ws, bands, s)) : MUON_OK;
+  }
+};
 
 // ---- RMS norm --------------------------------------------------------------------------
 muon_status_t norm_impl(const muon_rmsnorm_t* a, cudaStream_t stream) {
@@ -163,13 +185,17 @@ muon_status_t norm_grad_impl(const muon_rmsnorm_grad_t* a, cudaStream_t stream) 
   Counter c;
   p.status = d.status, p.timeout_ns = d.timeout_ns;
   const int slots = norm_grad_slots(p, d.sms);
+  Carve cv;
   if (a->dgain) {
-    char* ws = nullptr;
-    MUON_TRY(workspace(stream, static_cast<size_t>(slots) * p.cols * 4, &ws));
-    p.part = reinterpret_cast<float*>(ws);
+    cv.take(static_cast<int64_t>(slots) * p.cols * 4);
+    MUON_TRY(cv.open(stream));
+    p.part = reinterpret_cast<float*>(cv.ws);
   }
   MUON_TRY(c.run(launch_norm_grad(p, d.sms, stream)));
-  if (a->dgain) MUON_TRY(c.run(launch_norm_dgain(p.part, slots, p.cols, a->dgain, stream)));
+  if (a->dgain) {
+    MUON_TRY(c.run(launch_norm_dgain(p.part, slots, p.cols, a->dgain, stream)));
+    MUON_TRY(cv.close(stream));
+  }
   api_set_launches(c.n);
   return MUON_OK;
 }
@@ -193,6 +219,13 @@ bool unsupported_route(int64_t tokens, int top_k, int experts, int groups) {
 muon_status_t plan_launches(const PlanParams& p, Counter* c, cudaStream_t stream) {
   if (p.tiles > 1) MUON_TRY(c->run(launch_plan_hist(p, c->n > 0, stream)));
   return c->run(launch_plan(p, c->n > 0, stream));
+}
+
+muon_status_t plan_counts(PlanParams* p, Carve* cv, cudaStream_t stream) {
+  cv->take(static_cast<int64_t>(p->tiles) * p->experts * 4);
+  MUON_TRY(cv->open(stream));
+  p->hist = reinterpret_cast<int32_t*>(cv->ws);
+  return MUON_OK;
 }
 
 PlanParams plan_params(const int32_t* idx, int64_t tokens, int top_k, int experts, int32_t* offsets,
@@ -249,14 +282,13 @@ muon_status_t route_impl(const muon_route_config_t* cfg, const void* logits, int
   p.scale = cfg->scale;
   p.status = d.status;
   PlanParams pp = plan_params(idx, tokens, cfg->top_k, cfg->experts, offsets, src, pos);
-  if (offsets && pp.tiles > 1) {
-    char* ws = nullptr;
-    MUON_TRY(workspace(stream, static_cast<size_t>(pp.tiles) * cfg->experts * 4, &ws));
-    pp.hist = reinterpret_cast<int32_t*>(ws);
-  }
+  Carve cv;
+  const bool counts = offsets && pp.tiles > 1;
+  if (counts) MUON_TRY(plan_counts(&pp, &cv, stream));
   Counter c;
   MUON_TRY(c.run(launch_route(p, stream)));
   if (offsets) MUON_TRY(plan_launches(pp, &c, stream));
+  if (counts) MUON_TRY(cv.close(stream));
   api_set_launches(c.n);
   return MUON_OK;
 }
@@ -277,13 +309,11 @@ muon_status_t plan_impl(const int32_t* idx, int64_t tokens, int top_k, int exper
     return MUON_ERR_ALIAS;
   std::lock_guard<std::mutex> lock(api_mutex());
   PlanParams p = plan_params(idx, tokens, top_k, experts, offsets, src, pos);
-  if (p.tiles > 1) {
-    char* ws = nullptr;
-    MUON_TRY(workspace(stream, static_cast<size_t>(p.tiles) * experts * 4, &ws));
-    p.hist = reinterpret_cast<int32_t*>(ws);
-  }
+  Carve cv;
+  if (p.tiles > 1) MUON_TRY(plan_counts(&p, &cv, stream));
   Counter c;
   MUON_TRY(plan_launches(p, &c, stream));
+  if (p.tiles > 1) MUON_TRY(cv.close(stream));
   api_set_launches(c.n);
   return MUON_OK;
 }
@@ -360,16 +390,6 @@ bool experts_alias(const ExpertsViews& v, std::initializer_list<View> more_input
 }
 
 int64_t rup(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-
-// Workspace, cut into 256-byte aligned pieces: sizes first, then pointers.
-struct Carve {
-  size_t bytes = 0;
-  size_t take(int64_t n) {
-    const size_t at = bytes;
-    bytes += pad256(static_cast<size_t>(n));
-    return at;
-  }
-};
 
 // The weights as the tensor maps want them: rows of a multiple of 8 elements
 // on 16-byte boundaries, inner a multiple of 8 (gate and up rows interleave
@@ -578,28 +598,28 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
     // the SMs) against the weights' bytes per row.
     const int64_t ip = rup(I, 8);
     const size_t at = cv.take(rows * ip * 4);
-    char* ws = nullptr;
-    MUON_TRY(workspace(stream, cv.bytes, &ws));
+    MUON_TRY(cv.open(stream));
     ExFewParams p;
     std::memset(&p, 0, sizeof(p));
     p.x = static_cast<const __nv_bfloat16*>(a->x), p.xs = a->x_stride;
     p.w_in = static_cast<const __nv_bfloat16*>(a->w_in), p.w_out = static_cast<const __nv_bfloat16*>(a->w_out);
     p.weights = a->weights, p.offsets = a->offsets, p.src = a->src, p.pos = a->pos;
-    p.gu = static_cast<__nv_bfloat16*>(gu), p.act = reinterpret_cast<float*>(ws + at);
+    p.gu = static_cast<__nv_bfloat16*>(gu), p.act = reinterpret_cast<float*>(cv.ws + at);
     p.out = static_cast<__nv_bfloat16*>(out), p.outs = outs;
     p.tokens = a->tokens, p.ip = ip, p.rows = static_cast<int>(rows);
     p.hidden = static_cast<int>(H), p.inner = static_cast<int>(I), p.experts = a->experts, p.top_k = a->top_k;
     p.vec_in = v.x.rows16() && aligned(a->w_in, 16) && H % 8 == 0;
     p.vec_out = aligned(a->w_out, 16) && I % 8 == 0;
     MUON_TRY(c.run(launch_ex_few(p, stream)));
+    MUON_TRY(cv.close(stream));
     api_set_launches(2);
     return MUON_OK;
   }
   const WeightPlan w(a, &cv);
   const RowPlan rp(rows, H, &cv);
   const size_t at_x = cv.take(rows * w.hp * 2), at_act = cv.take(rows * w.ip * 2);
-  char* ws = nullptr;
-  MUON_TRY(workspace(stream, cv.bytes, &ws));
+  MUON_TRY(cv.open(stream));
+  char* const ws = cv.ws;
   __nv_bfloat16* xp = reinterpret_cast<__nv_bfloat16*>(ws + at_x);
   __nv_bfloat16* act = reinterpret_cast<__nv_bfloat16*>(ws + at_act);
   const __nv_bfloat16 *w_in, *w_out;
@@ -623,6 +643,7 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   MUON_TRY(c.run(launch_ex_gemm(kExUp, up, d.sms, early, stream)));
   MUON_TRY(c.run(launch_ex_gemm(kExDown, down, d.sms, early, stream)));
   MUON_TRY(c.run(launch_ex_combine(combine_params(a, down, a->weights, o), d.sms, early, stream)));
+  MUON_TRY(cv.close(stream));
   api_set_launches(c.n);
   return MUON_OK;
 }
@@ -665,8 +686,8 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   const size_t at_x = cv.take(prows * xpitch * 2), at_d = cv.take(prows * xpitch * 2), at_wr = cv.take(prows * 4),
                at_dgu = cv.take(prows * gpitch * 2), at_wa = cv.take(prows * apitch * 2),
                at_part = cv.take(rows * parts * 4);
-  char* ws = nullptr;
-  MUON_TRY(workspace(stream, cv.bytes, &ws));
+  MUON_TRY(cv.open(stream));
+  char* const ws = cv.ws;
   __nv_bfloat16* xp = reinterpret_cast<__nv_bfloat16*>(ws + at_x);
   __nv_bfloat16* dop = reinterpret_cast<__nv_bfloat16*>(ws + at_d);
   __nv_bfloat16* dgu = reinterpret_cast<__nv_bfloat16*>(ws + at_dgu);
@@ -737,6 +758,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
       return MUON_ERR_CUDA;
     MUON_TRY(c.run(launch_ex_gemm(k ? kExDwOut : kExDwIn, p, d.sms, early, stream)));
   }
+  MUON_TRY(cv.close(stream));
   api_set_launches(c.n);
   return MUON_OK;
 }
