@@ -371,6 +371,10 @@ muon_status_t muon_debug_guard_check(cudaStream_t stream, int64_t *bad_bytes);
  *     be used side by side; views of different pitches must not interleave.
  *   - 16-byte aligned pointers and strides of a multiple of 16 bytes are
  *     fastest; any element-aligned pointer and any stride works.
+ *   - After one call of the library on the device, a call may be captured in a
+ *     CUDA graph.  The graph then names the workspace of the capturing stream,
+ *     which lasts (outgrown or not) until muon_release_workspace; its runs must
+ *     not overlap calls on that stream or other graphs captured there.
  * ====================================================================== */
 
 /* h = x + residual (x alone when residual is NULL), in fp32;
@@ -550,7 +554,8 @@ muon_status_t muon_experts_backward(const muon_experts_t *args, const void *dout
 /* Static, human-readable name of a status code. */
 const char *muon_status_string(muon_status_t status);
 
-/* Free every cached workspace (synchronises the streams that own them). */
+/* Free every cached workspace (synchronises the streams that own them); graphs
+ * captured from the block's calls must not run afterwards. */
 void muon_release_workspace(void);
 
 /* Number of kernels the last successful call on this host thread enqueued. */

@@ -40,6 +40,8 @@ constexpr float kShiftFrac = 0.58f;   // alpha_k = 0.58 a_k (about 2 for the def
 struct Workspace {
   void* ptr = nullptr;
   size_t bytes = 0;
+  bool captured = false;         // a CUDA graph names ptr
+  std::vector<void*> retired;    // outgrown buffers that graphs name
   unsigned* ctr = nullptr;
   size_t ctr_bytes = 0;
   bool dirty = false;  // a kernel gave up mid-way: counters must be re-zeroed
@@ -496,6 +498,33 @@ std::vector<ChunkP> make_plan(const std::vector<Req>& reqs, int sms, bool precis
 }
 
 // ---- workspace ---------------------------------------------------------------------
+// Makes w.ptr at least `bytes` large (the stream is synchronised already unless
+// it is capturing).  A buffer that a graph names is kept until
+// muon_release_workspace: the graph may run again.
+muon_status_t grow_workspace(Workspace& w, size_t bytes, bool capturing) {
+  if (w.bytes >= bytes) return MUON_OK;
+  if (w.ptr) {
+    if (capturing || w.captured) w.retired.push_back(w.ptr);
+    else cudaFree(w.ptr);
+  }
+  w.ptr = nullptr;
+  w.bytes = 0;
+  w.captured = false;
+  const size_t want = align_up(bytes, size_t(1) << 21);
+  // an allocation is no part of the graph; a capture forbids it unless asked
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (capturing) cudaThreadExchangeStreamCaptureMode(&mode);
+  const cudaError_t e = cudaMalloc(&w.ptr, want);
+  if (capturing) cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    w.ptr = nullptr;
+    return MUON_ERR_OUT_OF_MEMORY;
+  }
+  w.bytes = want;
+  return MUON_OK;
+}
+
 muon_status_t get_workspace(cudaStream_t stream, size_t bytes, size_t ctrs, char** out,
                             unsigned** ctr_out) {
   int dev = 0;
@@ -505,18 +534,8 @@ muon_status_t get_workspace(cudaStream_t stream, size_t bytes, size_t ctrs, char
   if (w.bytes < bytes || w.ctr_bytes < ctr_bytes) {
     if (cudaStreamSynchronize(stream) != cudaSuccess) return MUON_ERR_CUDA;
   }
-  if (w.bytes < bytes) {
-    if (w.ptr) cudaFree(w.ptr);
-    w.ptr = nullptr;
-    w.bytes = 0;
-    const size_t want = align_up(bytes, size_t(1) << 21);
-    if (cudaMalloc(&w.ptr, want) != cudaSuccess) {
-      cudaGetLastError();
-      w.ptr = nullptr;
-      return MUON_ERR_OUT_OF_MEMORY;
-    }
-    w.bytes = want;
-  }
+  const muon_status_t st = grow_workspace(w, bytes, false);
+  if (st != MUON_OK) return st;
   if (w.ctr_bytes < ctr_bytes) {
     if (w.ctr) cudaFree(w.ctr);
     w.ctr = nullptr;
@@ -1532,8 +1551,21 @@ int api_device(ApiDevice* out) {
 }
 
 int api_workspace(cudaStream_t stream, size_t bytes, char** out) {
-  unsigned* ctr = nullptr;
-  return get_workspace(stream, bytes, 1, out, &ctr);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MUON_ERR_CUDA;
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
+    cudaGetLastError();
+    return MUON_ERR_CUDA;
+  }
+  const bool capturing = cs != cudaStreamCaptureStatusNone;
+  Workspace& w = g_ws[{dev, stream}];
+  if (w.bytes < bytes && w.ptr && !capturing && cudaStreamSynchronize(stream) != cudaSuccess) return MUON_ERR_CUDA;
+  const muon_status_t st = grow_workspace(w, bytes, capturing);
+  if (st != MUON_OK) return st;
+  w.captured = w.captured || capturing;
+  *out = static_cast<char*>(w.ptr);
+  return MUON_OK;
 }
 
 size_t api_guard_bytes() { return env_size("MUON_WS_GUARD", 0) ? kGuardBytes : 0; }
@@ -1748,10 +1780,11 @@ void muon_release_workspace(void) {
     int cur = 0;
     cudaGetDevice(&cur);
     for (auto& kv : g_ws) {
-      if (kv.second.ptr || kv.second.ctr) {
+      if (kv.second.ptr || kv.second.ctr || !kv.second.retired.empty()) {
         cudaSetDevice(kv.first.first);
         cudaStreamSynchronize(kv.first.second);
         if (kv.second.ptr) cudaFree(kv.second.ptr);
+        for (void* p : kv.second.retired) cudaFree(p);
         if (kv.second.ctr) cudaFree(kv.second.ctr);
       }
     }
