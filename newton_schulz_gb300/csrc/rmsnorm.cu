@@ -359,6 +359,16 @@ __device__ __forceinline__ bool ring_wait(uint64_t* full, uint32_t parity, unsig
   return !__syncthreads_or(!wait_bounded(full, parity, status, timeout_ns));
 }
 
+// After a wait that gave up at stage s: the copies still on their way (of `left`
+// rows at most) end before the block's memory does.
+__device__ __noinline__ void ring_drain(uint64_t* full, int stages, int s, uint32_t phase, int64_t left,
+                                        unsigned* status, unsigned long long timeout_ns) {
+  for (int k = 0; k < stages && k < left; ++k) {
+    const int at = s + k < stages ? s + k : s + k - stages;
+    wait_bounded(&full[at], phase ^ (s + k < stages ? 0u : 1u), status, timeout_ns);
+  }
+}
+
 // Gradient: row slot s takes rows s, s + slots, ...; its share of dgain stays
 // in registers until the end.
 template <int NV, bool WIDE>
@@ -498,9 +508,11 @@ __global__ void __launch_bounds__(256, 2)
   }
   int s = 0, par = 0;
   uint32_t phase = 0;
-  int64_t row = blockIdx.x;
-  for (; row < rows; row += step) {
-    if (!ring_wait(&full[s], phase, p.status, p.timeout_ns)) break;
+  for (int64_t row = blockIdx.x; row < rows; row += step) {
+    if (!ring_wait(&full[s], phase, p.status, p.timeout_ns)) {
+      if (t == 0) ring_drain(full, stages, s, phase, (rows - 1 - row) / step + 1, p.status, p.timeout_ns);
+      break;
+    }
     const uint8_t* d = ring + s * pitch;
     Chunk<WIDE> cd[NV], ch[NV], cs[NV];
     float2 ss2 = make_float2(0.f, 0.f), dot2 = ss2;
@@ -555,12 +567,6 @@ __global__ void __launch_bounds__(256, 2)
       store_chunk(out, p.dh_dt, col, p.cols, true, v);
     }
   }
-  // gave up: the copies still on their way end before the block's memory does
-  if (t == 0)
-    for (int k = 0; k < stages && row + static_cast<int64_t>(k) * step < rows; ++k) {
-      const int at = s + k < stages ? s + k : s + k - stages;
-      wait_bounded(&full[at], phase ^ (s + k < stages ? 0u : 1u), p.status, p.timeout_ns);
-    }
   if (p.part) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
