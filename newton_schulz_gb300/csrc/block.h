@@ -75,6 +75,7 @@ struct NormParams {
   int n_scales;                       // scales per row
   int vec;                            // 16-byte accesses are legal
   float eps, inv_cols;                // inv_cols = 1 / cols
+  unsigned* status;
 };
 
 struct NormGradParams {
@@ -128,6 +129,7 @@ struct RouteGradParams {
   int experts, top_k, score, renorm;
   int vec, dvec;                  // 16-byte aligned rows of logits, dlogits
   float scale;
+  unsigned* status;
 };
 
 struct PlanParams {
@@ -139,6 +141,7 @@ struct PlanParams {
   int32_t* offsets;
   int32_t* src;
   int32_t* pos;
+  unsigned* status;
 };
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t s);
@@ -165,6 +168,7 @@ struct ExGemmParams {
   CUtensorMap mapB32;             // token rows in boxes of 32 (kExDw*: unused)
   const int32_t* offsets;         // [experts + 1]
   int64_t rows;                   // tokens * top_k, the most rows there are
+  int64_t prows;                  // the same in the padded numbering
   int experts;
   int beside;                     // 1: runs beside the previous launch, whose results it does not use
   int pad;                        // padded row numbering: segments of 1 or kExSeg rows
@@ -205,6 +209,8 @@ struct ExSpreadParams {
   const int32_t* offsets;
   const int32_t* pos;
   int64_t tokens, rows, hidden, hp;
+  int64_t prows;                  // rows of out
+  unsigned* status;
   int experts, top_k, pad;
   int span;                       // columns a warp takes at a time (set at the launch)
   int beside;                     // 1: runs beside the previous launch, whose results it does not use
@@ -247,6 +253,7 @@ struct ExFewParams {
   int64_t outs, tokens, ip;
   int hidden, inner, experts, top_k, rows;
   int vec_in, vec_out;            // 16-byte loads of x and w_in, of w_out
+  unsigned* status;
 };
 cudaError_t launch_ex_few(const ExFewParams& p, cudaStream_t s);    // two launches
 

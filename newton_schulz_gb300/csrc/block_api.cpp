@@ -133,6 +133,7 @@ muon_status_t norm_impl(const muon_rmsnorm_t* a, cudaStream_t stream) {
   std::lock_guard<std::mutex> lock(api_mutex());
   ApiDevice d;
   MUON_TRY(device(&d));
+  p.status = d.status;
   Counter c;
   MUON_TRY(c.run(launch_norm(p, d.sms, stream)));
   api_set_launches(c.n);
@@ -282,6 +283,7 @@ muon_status_t route_impl(const muon_route_config_t* cfg, const void* logits, int
   p.scale = cfg->scale;
   p.status = d.status;
   PlanParams pp = plan_params(idx, tokens, cfg->top_k, cfg->experts, offsets, src, pos);
+  pp.status = d.status;
   Carve cv;
   const bool counts = offsets && pp.tiles > 1;
   if (counts) MUON_TRY(plan_counts(&pp, &cv, stream));
@@ -308,7 +310,10 @@ muon_status_t plan_impl(const int32_t* idx, int64_t tokens, int top_k, int exper
   if (i.overlaps(o) || i.overlaps(s) || i.overlaps(q) || o.overlaps(s) || o.overlaps(q) || s.overlaps(q))
     return MUON_ERR_ALIAS;
   std::lock_guard<std::mutex> lock(api_mutex());
+  ApiDevice d;
+  MUON_TRY(device(&d));
   PlanParams p = plan_params(idx, tokens, top_k, experts, offsets, src, pos);
+  p.status = d.status;
   Carve cv;
   if (p.tiles > 1) MUON_TRY(plan_counts(&p, &cv, stream));
   Counter c;
@@ -343,6 +348,9 @@ muon_status_t route_grad_impl(const muon_route_config_t* cfg, const void* logits
   p.vec = l.rows16(), p.dvec = o.rows16();
   p.scale = cfg->scale;
   std::lock_guard<std::mutex> lock(api_mutex());
+  ApiDevice d;
+  MUON_TRY(device(&d));
+  p.status = d.status;
   Counter c;
   MUON_TRY(c.run(launch_route_grad(p, stream)));
   api_set_launches(c.n);
@@ -521,12 +529,12 @@ int pairs_for(const muon_experts_t* a, int64_t rows, int64_t m_rows, int64_t k) 
   return rows >= int64_t{256} * a->experts && k >= 1024 && (m_tiles % 2 == 0 || m_tiles >= 9) ? 2 : 1;
 }
 
-ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const ApiDevice& d, int pad, int64_t m_rows,
-                         int pairs) {
+ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const ApiDevice& d, int pad, int64_t prows,
+                         int64_t m_rows, int pairs) {
   ExGemmParams p;
   std::memset(&p, 0, sizeof(p));
   p.offsets = a->offsets;
-  p.rows = a->tokens * a->top_k;
+  p.rows = a->tokens * a->top_k, p.prows = prows;
   p.experts = a->experts;
   p.pad = pad;
   p.pairs = pairs;
@@ -537,13 +545,15 @@ ExGemmParams gemm_params(const muon_experts_t* a, const WeightPlan& w, const Api
   return p;
 }
 
-ExSpreadParams spread_params(const muon_experts_t* a, const WeightPlan& w, int pad) {
+ExSpreadParams spread_params(const muon_experts_t* a, const WeightPlan& w, const ApiDevice& d, int pad,
+                             int64_t prows) {
   ExSpreadParams g;
   std::memset(&g, 0, sizeof(g));
   g.x = static_cast<const __nv_bfloat16*>(a->x), g.xs = a->x_stride;
   g.offsets = a->offsets, g.pos = a->pos;
   g.tokens = a->tokens, g.rows = a->tokens * a->top_k, g.hidden = a->hidden, g.hp = w.hp;
   g.experts = a->experts, g.top_k = a->top_k, g.pad = pad;
+  g.prows = prows, g.status = d.status;
   return g;
 }
 
@@ -610,6 +620,7 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
     p.hidden = static_cast<int>(H), p.inner = static_cast<int>(I), p.experts = a->experts, p.top_k = a->top_k;
     p.vec_in = v.x.rows16() && aligned(a->w_in, 16) && H % 8 == 0;
     p.vec_out = aligned(a->w_out, 16) && I % 8 == 0;
+    p.status = d.status;
     MUON_TRY(c.run(launch_ex_few(p, stream)));
     MUON_TRY(cv.close(stream));
     api_set_launches(2);
@@ -625,16 +636,16 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   const __nv_bfloat16 *w_in, *w_out;
   MUON_TRY(pack_weights(a, w, ws, &w_in, &w_out, &c, stream));
   const bool early = rows <= kEarlyRows;
-  ExSpreadParams g = spread_params(a, w, 1);
+  ExSpreadParams g = spread_params(a, w, d, 1, rows);
   g.out = xp;
   g.vec = v.x.rows16();
   MUON_TRY(c.run(launch_ex_spread(g, kSpreadBlocks * d.sms, stream)));
-  ExGemmParams up = gemm_params(a, w, d, 1, 2 * w.ip, pairs_for(a, rows, 2 * w.ip, H));
+  ExGemmParams up = gemm_params(a, w, d, 1, rows, 2 * w.ip, pairs_for(a, rows, 2 * w.ip, H));
   up.kb = tiles_of(H, 64), up.m = up.inner;
   up.act = act;
   up.gu = static_cast<__nv_bfloat16*>(gu);
   up.gu_vec = aligned(gu, 16) && I % 8 == 0;
-  ExGemmParams down = gemm_params(a, w, d, 1, H, pairs_for(a, rows, H, I));
+  ExGemmParams down = gemm_params(a, w, d, 1, rows, H, pairs_for(a, rows, H, I));
   down.kb = tiles_of(I, 64), down.m = static_cast<int>(H);
   rp.set(&down, ws);
   if (!map_up(&up.mapA, w_in, a, w) || !map_rows(&up, xp, H, rows, w.hp) ||
@@ -695,7 +706,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   Counter c;
   const __nv_bfloat16 *w_in, *w_out;
   MUON_TRY(pack_weights(a, w, ws, &w_in, &w_out, &c, stream));
-  ExSpreadParams g = spread_params(a, w, kExSeg);
+  ExSpreadParams g = spread_params(a, w, d, kExSeg, prows);
   g.hp = xpitch;
   g.x = static_cast<const __nv_bfloat16*>(dout), g.xs = dos, g.out = dop;
   g.vec = vd.rows16();
@@ -718,7 +729,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   };
   float* const wr = g.wr;
   if (dw_in && !beside) MUON_TRY(copy_x(kSpreadBlocks, true));
-  ExGemmParams da = gemm_params(a, w, d, kExSeg, I, 1);
+  ExGemmParams da = gemm_params(a, w, d, kExSeg, prows, I, 1);
   da.kb = tiles_of(H, 64), da.m = da.inner;
   da.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));
   da.gu_vec = aligned(gu, 16) && I % 8 == 0;
@@ -734,7 +745,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
   }
   if (beside) MUON_TRY(copy_x(1, false));
   if (dx) {
-    ExGemmParams p = gemm_params(a, w, d, kExSeg, H, pairs_for(a, prows, H, 2 * I));
+    ExGemmParams p = gemm_params(a, w, d, kExSeg, prows, H, pairs_for(a, prows, H, 2 * I));
     p.beside = beside;
     p.kb = tiles_of(2 * w.ip, 64), p.m = static_cast<int>(H);
     rp.set(&p, ws);
@@ -747,7 +758,7 @@ muon_status_t experts_grad_impl(const muon_experts_t* a, const void* dout, int64
     void* out = k ? dw_out : dw_in;
     if (!out) continue;
     const int64_t m = k ? H : 2 * w.ip;
-    ExGemmParams p = gemm_params(a, w, d, kExSeg, m, pairs_for(a, prows, m, prows / a->experts));
+    ExGemmParams p = gemm_params(a, w, d, kExSeg, prows, m, pairs_for(a, prows, m, prows / a->experts));
     p.m = static_cast<int>(m), p.n = static_cast<int>(k ? I : H);
     p.n_tiles = tiles_of(p.n, kExNTile);
     p.dw = out, p.dw_dt = dw_dt;

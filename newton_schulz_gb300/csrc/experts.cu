@@ -206,6 +206,16 @@ __device__ __forceinline__ Tile decode(const ExGemmParams& p, const Scan& s, int
   return t;
 }
 
+// Debug builds: the tile's indices, and the rows that its copies and stores touch.
+template <int KIND>
+__device__ __forceinline__ bool tile_in_range(const ExGemmParams& p, const Tile& t) {
+  const bool place = t.e >= 0 && t.e < p.experts && t.m >= 0 && t.m < p.m_tiles && t.prow >= 0 && t.kb >= 0;
+  if (is_dw(KIND)) return place && t.n >= 0 && t.n < p.n_tiles && t.prow + static_cast<int64_t>(t.kb) * BK <= p.prows;
+  return place && t.urow >= 0 && t.valid >= 0 && t.valid <= t.rows && t.rows <= t.cols && t.cols <= kExNTile &&
+         t.cols % 32 == 0 && t.prow + static_cast<int64_t>(t.rows) <= p.prows &&
+         t.urow + static_cast<int64_t>(t.valid) <= p.rows;
+}
+
 // A warp's tiles in order, decoded 32 at a time, one by each lane: decoding (a
 // search of the offsets and four divisions, about 1200 cycles) once per tile in
 // the copies' and the MMAs' threads cost a fifth of a tile of 12 K blocks.
@@ -651,6 +661,7 @@ __device__ __forceinline__ void epi_dw(const ExGemmParams& p, const Tile& t, con
       if (!ok || col >= p.n) continue;
       const uint4 v = lds16(staged(w.stg, rr, chunk, 128));
       const int64_t at = (t.e * m_out + m) * p.n + col;
+      if (!dbg_ok(at + min(per, p.n - col) <= p.experts * m_out * p.n, p.status)) continue;
       if (!f32) {
         store8(static_cast<__nv_bfloat16*>(p.dw) + at, v, p.n - col, p.dw_vec != 0);
       } else {
@@ -738,6 +749,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThread
     const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), rank & ~1);
     for (int tile = tile0, it = 0; tile < tiles && !stop; tile += tstep, ++it) {
       const Tile t = feed.get(p, scan, tiles, tile0, tstep, it, lane);
+      if (!dbg_ok(tile_in_range<KIND>(p, t), p.status)) break;      // consumers time out
       // B: 128 rows in boxes of 128 / PAIRS, one from each pair for all; for a
       // small tile one or two boxes of 32
       const int half = t.cols / 2, small = half > 64 ? 0 : (half + 31) / 32;
@@ -873,6 +885,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThread
     Feed<KIND> feed;
     for (int tile = tile0, it = 0; tile < tiles; tile += tstep, ++it) {
       const Tile t = feed.get(p, scan, tiles, tile0, tstep, it, lane);
+      if (!dbg_ok(tile_in_range<KIND>(p, t), p.status)) break;
       w.m0 = m_first(t);
       const int buf = acc & 1;
       w.taddr = tmem + buf * 256 + (static_cast<uint32_t>(w.q4 * 32) << 16);
@@ -941,12 +954,13 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
   for (int64_t tok = first; tok < tokens; tok += step) {
     int row = next < total ? next : -1;
     next = slot(tok + step);
-    const unsigned live = __ballot_sync(kFull, row >= 0);
-    if (!live) continue;
     if (p.pad > 1 && row >= 0) {
       const int e = find(s.off, p.experts, row);
       row += s.poff[e] - s.off[e];
     }
+    if (!dbg_ok(row < p.prows, p.status)) row = -1;
+    const unsigned live = __ballot_sync(kFull, row >= 0);
+    if (!live) continue;
     const __nv_bfloat16* in = p.x + tok * p.xs;
     for (int cb = begin; cb < end; cb += 2048) {
       const int c0 = cb + lane * 8;
@@ -968,7 +982,7 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
   // zeros after each expert's rows
   for (int i = first; p.pad > 1 && i < p.experts * p.pad; i += step) {
     const int e = i / p.pad, r = s.poff[e] + s.off[e + 1] - s.off[e] + i % p.pad;
-    if (r >= s.poff[e + 1]) continue;
+    if (r >= s.poff[e + 1] || !dbg_ok(r < p.prows, p.status)) continue;
     for (int c = begin + lane * 8; c < end; c += 256)
       *reinterpret_cast<uint4*>(p.out + r * p.hp + c) = make_uint4(0u, 0u, 0u, 0u);
     if (p.wr && lane == 0 && begin == 0) p.wr[r] = 0.f;

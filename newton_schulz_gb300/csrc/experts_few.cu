@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kWarps * 32) ex_few_up_kernel(const __grid_con
   const int32_t s = p.src[row];
   const int e = ends.expert(row, p.experts);
   if (e >= p.experts || s < 0 || s >= p.rows) return;      // past the last row
+  if (!dbg_ok(ft < p.inner && s / p.top_k < p.tokens && ft < p.ip, p.status)) return;
   const __nv_bfloat16* x = p.x + (s / p.top_k) * p.xs;
   const __nv_bfloat16* g = p.w_in + (static_cast<int64_t>(e) * 2 * p.inner + ft) * p.hidden;
   const __nv_bfloat16* v = g + static_cast<int64_t>(p.inner) * p.hidden;
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kWarps * 32) ex_few_down_kernel(const __grid_c
     my_row = -1;
     my_e = 0;
   }
+  if (!dbg_ok(h < p.hidden && t < p.tokens, p.status)) return;
   float acc = 0.f;
   constexpr int kSlots = 4;
   for (int j0 = 0; j0 < p.top_k; j0 += kSlots) {

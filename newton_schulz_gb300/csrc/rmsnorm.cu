@@ -321,6 +321,10 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 8 ? 512 : 256, NV == 2 
   const int64_t row = live ? row_raw : p.rows - 1;
   const bool vec = p.vec != 0;
   const bool has_res = p.r_dt != kDtNone;
+  // a row's chunks cover it, and its threads are one warp's or the block's
+  if (!dbg_ok(row >= 0 && static_cast<int64_t>(NV) * tpr * 8 >= p.cols &&
+                  (tpr <= 32 ? 32 % tpr == 0 : tpr == static_cast<int>(blockDim.x)), p.status))
+    return;
   const char* xr = row_ptr(p.x, p.x_dt, row, p.xs);
   const char* rr = has_res ? row_ptr(p.res, p.r_dt, row, p.rs) : xr;
   Chunk<WIDE> cx[NV], cr[NV];
@@ -358,7 +362,6 @@ __device__ __forceinline__ bool ring_wait(uint64_t* full, uint32_t parity, unsig
                                           unsigned long long timeout_ns) {
   return !__syncthreads_or(!wait_bounded(full, parity, status, timeout_ns));
 }
-
 // After a wait that gave up at stage s: the copies still on their way (of `left`
 // rows at most) end before the block's memory does.
 __device__ __noinline__ void ring_drain(uint64_t* full, int stages, int s, uint32_t phase, int64_t left,
@@ -381,6 +384,9 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : NV == 8 ? 512 : 256, NV == 2 
   const int slots = gridDim.x * per;
   const bool vec = p.vec != 0;
   const bool has_res = p.dr_dt != kDtNone;
+  if (!dbg_ok(static_cast<int64_t>(NV) * tpr * 8 >= p.cols &&
+                  (tpr <= 32 ? 32 % tpr == 0 : tpr == static_cast<int>(blockDim.x)), p.status))
+    return;
   float acc[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -482,7 +488,12 @@ __global__ void __launch_bounds__(256, 2)
   auto fetch = [&](int64_t row, int s) {
     uint8_t* d = ring + s * pitch;
     ptx::mbar_arrive_expect_tx(&full[s], bytes);
-    if (p.inject && row == 0) return;      // testing hook: the wait for row 0 runs out
+    if (!dbg_ok(row < rows && s < stages && stages <= kNormStages && stages * pitch <= kNormRingBytes &&
+                    ((reinterpret_cast<uintptr_t>(row_ptr(p.dy, p.dy_dt, row, p.dys)) |
+                      reinterpret_cast<uintptr_t>(row_ptr(p.h, p.h_dt, row, p.hs)) |
+                      reinterpret_cast<uintptr_t>(has_res ? row_ptr(p.dres, p.dr_dt, row, p.drs) : nullptr) |
+                      bd | bh | bs) & 15) == 0, p.status))
+      return;                              // the wait for it runs out
     ptx::bulk_load(d, row_ptr(p.dy, p.dy_dt, row, p.dys), bd, &full[s]);
     ptx::bulk_load(d + bd, row_ptr(p.h, p.h_dt, row, p.hs), bh, &full[s]);
     if (has_res) ptx::bulk_load(d + bd + bh, row_ptr(p.dres, p.dr_dt, row, p.drs), bs, &full[s]);
@@ -494,7 +505,8 @@ __global__ void __launch_bounds__(256, 2)
   __syncthreads();
   if (t == 0)
     for (int s = 0; s < stages; ++s)
-      if (blockIdx.x + static_cast<int64_t>(s) * step < rows) fetch(blockIdx.x + s * step, s);
+      if (p.inject && blockIdx.x == 0 && s == 0) ptx::mbar_arrive_expect_tx(&full[0], bytes);   // testing hook
+      else if (blockIdx.x + static_cast<int64_t>(s) * step < rows) fetch(blockIdx.x + s * step, s);
   float2 acc[NV][4], g[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {

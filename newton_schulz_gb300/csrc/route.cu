@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     const float total = warp_sum(my_score);   // lanes from top_k on hold 0
     my_score = total > 0.f ? my_score / total : 0.f;
   }
-  if (lane < k) {
+  if (lane < k && dbg_ok(my_idx >= -1 && my_idx < p.experts, p.status)) {
     p.idx[tok * k + lane] = my_idx;
     p.weights[tok * k + lane] = my_score * p.scale;
   }
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   for (int i = 0; i < EPL; ++i) mine[i] = 0.f;
   s_chosen[warp][lane] = 0u;
   __syncwarp();
-  if (e >= 0 && e < p.experts) {
+  if (e >= 0 && e < p.experts && dbg_ok(e / EPL < 32, p.status)) {
     s_d[warp][e / EPL * kPitch + e % EPL] = dw;
     atomicOr(&s_chosen[warp][e / EPL], 1u << (e % EPL));
   }
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __syncwarp();
     if (i < w1) {
       p.pos[i] = row;
-      if (row >= 0) p.src[row] = static_cast<int32_t>(i);
+      if (row >= 0 && dbg_ok(row < total, p.status)) p.src[row] = static_cast<int32_t>(i);
     }
   }
   // entries past the last row
