@@ -561,10 +561,12 @@ void muon_release_workspace(void);
 /* Number of kernels the last successful call on this host thread enqueued. */
 int muon_last_launch_count(void);
 
-/* Kernel-time accounting for measurement.  When enabled, each library launch
- * is bracketed by CUDA events on its stream; muon_profile_read (after the
- * stream is synchronised) adds the elapsed milliseconds per kernel kind into
- * ms[0..n) and launch counts into launches[0..n) and resets the record.
+/* Kernel-time accounting for measurement.  When enabled, each launch of the
+ * optimizer's entry points is bracketed by CUDA events on its stream (those of
+ * the mixture-of-experts block are counted by muon_last_launch_count only);
+ * muon_profile_read (after the stream is synchronised) adds the elapsed
+ * milliseconds per kernel kind into ms[0..n) and launch counts into
+ * launches[0..n) and resets the record.
  * Kinds: 0 prep (momentum/norm/cast/transpose), 1 Gram, 2 polynomial,
  * 3 apply, 4 update/copy-back, 5 fused small-m step, 6 AdamW.  Returns the
  * number of kinds (7). */
