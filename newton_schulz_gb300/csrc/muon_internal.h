@@ -179,6 +179,9 @@ constexpr int kGsR = 0, kGsT = 1, kGsB = 2, kGsQ0 = 3;   // Q ping-pong: kGsQ0, 
 // byte strides strides[0] (rows) and strides[1] (matrices).
 bool encode_tiled(CUtensorMap* map, bool f32, const void* base, const uint64_t* dims,
                   const uint64_t* strides, const uint32_t* box, bool swizzle128);
+// The same of rank 2 to 5; strides[i] is dimension i + 1's.
+bool encode_tiled_nd(CUtensorMap* map, bool f32, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box, bool swizzle128);
 // bf16, 128-byte swizzle, box {64, box_rows, 1}.
 bool make_ns_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t cnt,
                  int64_t pitch, int64_t mstride, int box_rows);
