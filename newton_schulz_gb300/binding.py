@@ -223,10 +223,8 @@ def _dtype_code(t) -> int:
 
 def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
-        # the handle alone: torch.cuda.current_stream() builds a Stream object,
-        # several microseconds of a small call
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -486,6 +484,17 @@ def _rows(t, name: str, cols: Optional[int] = None, rows: Optional[int] = None):
     return t.data_ptr(), stride, _code(t.dtype)
 
 
+def _current_handle() -> int:
+    """The current stream's handle.  torch.cuda.current_stream() builds a Stream
+    object, several microseconds of a small call; where torch has no cheaper
+    way to the handle, it is taken from there."""
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
+
+
 def _as_current(stream):
     """Context in which `stream` (a torch stream or a raw handle) is the current
     one.  The block's calls allocate their outputs in it: memory of another
@@ -550,7 +559,7 @@ def muon_rmsnorm_forward(x, gain=None, residual=None, eps: float = 1e-6, y_dtype
     else:
         scales = None
     a = RmsNorm(rows, cols, xp, xs, rp, rs, gp, hp, hs, yp, ys, sp, xc, rc, gc, hc, yc, group, eps)
-    check(load().muon_rmsnorm_forward(a, _stream_ptr(None)), "muon_rmsnorm_forward")
+    check(load().muon_rmsnorm_forward(a, _current_handle()), "muon_rmsnorm_forward")
     return y, h, scales
 
 
@@ -580,7 +589,7 @@ def muon_rmsnorm_backward(dy, h, gain=None, dres=None, eps: float = 1e-6, dh=Non
     if dgain is not None:
         wp = _dense(dgain, "dgain", (cols,), torch.float32)
     a = RmsNormGrad(rows, cols, dp, ds, hp, hs, gp, rp, rs, op, os_, wp, dc, hc, gc, rc, oc, eps)
-    check(load().muon_rmsnorm_backward(a, _stream_ptr(None)), "muon_rmsnorm_backward")
+    check(load().muon_rmsnorm_backward(a, _current_handle()), "muon_rmsnorm_backward")
     return dh, dgain
 
 
@@ -622,7 +631,7 @@ def muon_route_forward(logits, cfg: RouteConfig, bias=None, mask=None, plan: boo
     if mask is not None:
         m = _dense(mask, "mask", (tokens,), torch.bool if mask.dtype == torch.bool else torch.uint8)
     check(load().muon_route_forward(cfg, ptr, code, stride, tokens, b, m, idx.data_ptr(),
-                                    weights.data_ptr(), op, sp, pp, _stream_ptr(None)),
+                                    weights.data_ptr(), op, sp, pp, _current_handle()),
           "muon_route_forward")
     return Route(idx, weights, off, src, pos)
 
@@ -637,7 +646,7 @@ def muon_route_plan(idx, experts: int, stream=None):
     p = _dense(idx, "idx", (tokens, top_k), torch.int32)
     off, src, pos = _plan_tensors(idx.device, tokens, top_k, experts)
     check(load().muon_route_plan(p, tokens, top_k, experts, off.data_ptr(), src.data_ptr(),
-                                 pos.data_ptr(), _stream_ptr(None)), "muon_route_plan")
+                                 pos.data_ptr(), _current_handle()), "muon_route_plan")
     return off, src, pos
 
 
@@ -657,7 +666,7 @@ def muon_route_backward(logits, cfg: RouteConfig, idx, dweights, dlogits=None, s
     i = _dense(idx, "idx", (tokens, cfg.top_k), torch.int32)
     w = _dense(dweights, "dweights", (tokens, cfg.top_k), torch.float32)
     check(load().muon_route_backward(cfg, ptr, code, stride, tokens, i, w, dptr, dstride,
-                                     _stream_ptr(None)), "muon_route_backward")
+                                     _current_handle()), "muon_route_backward")
     return dlogits
 
 
@@ -702,7 +711,7 @@ def muon_experts_forward(x, w_in, w_out, route: Route, save: bool = False, out=N
     if save:
         gu = torch.empty((a.tokens * a.top_k, 2 * a.inner), dtype=torch.bfloat16, device=x.device)
     check(load().muon_experts_forward(a, optr, ostride,
-                                      gu.data_ptr() if save else None, _stream_ptr(None)),
+                                      gu.data_ptr() if save else None, _current_handle()),
           "muon_experts_forward")
     return out, gu
 
@@ -741,5 +750,5 @@ def muon_experts_backward(dout, x, w_in, w_out, route: Route, gu, dw_dtype=None,
         a, dptr, dstride, g, xptr, xstride,
         _dense(dw_in, "dw_in", w_in.shape, dw_dtype) if want_dw else None,
         _dense(dw_out, "dw_out", w_out.shape, dw_dtype) if want_dw else None,
-        code, dweights.data_ptr(), _stream_ptr(None)), "muon_experts_backward")
+        code, dweights.data_ptr(), _current_handle()), "muon_experts_backward")
     return dx, dw_in, dw_out, dweights

@@ -59,3 +59,13 @@ def test_raw_handles_and_positional_streams():
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for g in got)
     assert all(torch.equal(a, b) for a, b in zip(*plans))
+
+
+def test_current_handle(monkeypatch):
+    side = torch.cuda.Stream()
+    for drop in (False, True):          # with and without torch's direct way to the handle
+        if drop:
+            monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+        assert B._current_handle() == torch.cuda.current_stream().cuda_stream
+        with torch.cuda.stream(side):
+            assert B._current_handle() == side.cuda_stream
