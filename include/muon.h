@@ -331,8 +331,8 @@ int muon_debug_build(void);
  *   what = 1  the next grouped-GEMM launch (matrices with min(M,N) > 64, or
  *             the allocation-free entry point): one CTA never arms one
  *             pipeline stage, and its MMA issuer's wait on it runs out; the
- *             same for the next product of muon_experts_forward (more than 32
- *             (token, slot) pairs) or muon_experts_backward; or the next
+ *             same for the next product of muon_experts_backward, or of
+ *             muon_experts_forward beyond a few (token, slot) pairs; or the next
  *             muon_rmsnorm_backward through a ring of bulk copies (many rows
  *             of 520 to 8192 columns): a row's copies are never issued;
  *   what = 2  the next small-m launch (min(M,N) <= 64): the launch's last
@@ -509,8 +509,9 @@ muon_status_t muon_route_backward(const muon_route_config_t *cfg, const void *lo
  *   w_out  bf16 [experts, hidden, inner]
  *   weights, offsets, src, pos   as muon_route_forward wrote them
  * Products accumulate in fp32; the activation is rounded to bf16 once (it is
- * the next product's operand on the tensor cores; at most 32 (token, slot)
- * pairs are computed in fp32 throughout).  A slot's product, a term of the sum over slots
+ * the next product's operand on the tensor cores; a few (token, slot) pairs, at
+ * most 32, that hardly share experts are computed in fp32 throughout).  A slot's
+ * product, a term of the sum over slots
  * (its weight comes after), is kept as 16-bit floats with one exponent per 32
  * columns, within 2^-11 of itself or 2^-39 of the largest magnitude of its 32
  * columns, or in fp32 for those few rows; an infinity or NaN stays in its column.

@@ -237,7 +237,7 @@ struct ExWeightParams {           // dweights[t,j] = sum over parts of part[.][p
 };
 
 // A few rows: matrix-vector products, two launches, no padding or copies.
-constexpr int kExFewRows = 32;
+constexpr int kExFewRows = 32;    // most of them; few_rows (block_api.cpp) has the rule
 struct ExFewParams {
   const __nv_bfloat16* x;
   int64_t xs;

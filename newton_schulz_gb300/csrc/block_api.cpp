@@ -553,6 +553,22 @@ struct RowPlan {
   }
 };
 
+// Whether the matrix-vector kernels take a call.  They save the tile kernels'
+// launches, copy and sum, about 12 us, but read an expert's weights once for each
+// of its rows.  The host does not know the counts: it takes the experts that a
+// uniform routing hits on average, and up to 64 MB read twice, which is 11 us.
+// Matrix-vector against tiles, us: one token through 8 of 256 x [768, 2048] 23 / 37,
+// four 67 / 70; 2 of 8 x [768, 2048], 4 tokens 23 / 30, 8 tokens 39 / 31, 16 tokens
+// 67 / 31; 2 of 8 x [14336, 4096], one token 134 / 156, two 254 / 214, 16 tokens
+// 1824 / 444; 32 rows of one [512, 1024] 42 / 24, 16 rows 23 / 24.
+bool few_rows(const muon_experts_t* a) {
+  const int64_t rows = a->tokens * a->top_k;
+  if (rows > kExFewRows) return false;
+  const double share = std::min(1.0, static_cast<double>(a->top_k) / a->experts);
+  const double hit = a->experts * (1.0 - std::pow(1.0 - share, static_cast<double>(a->tokens)));
+  return (rows - hit) * 6.0 * static_cast<double>(a->hidden) * static_cast<double>(a->inner) <= 64e6;
+}
+
 constexpr int64_t kEarlyRows = 4096;  // most rows whose kernels are short: see launch_after
 constexpr int kSpreadBlocks = 5;      // per SM, for a copy that runs alone
 
@@ -573,9 +589,7 @@ muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, voi
   MUON_TRY(device(&d));
   Carve cv;
   Counter c;
-  if (rows <= kExFewRows) {
-    // The tile kernels' latency (launches, a ring to fill, tiles for a part of
-    // the SMs) against the weights' bytes per row.
+  if (few_rows(a)) {
     const int64_t ip = rup(I, 8);
     const size_t at = cv.take(rows * ip * 4);
     MUON_TRY(cv.open(stream));

@@ -1,7 +1,8 @@
 // The experts' forward products for a few rows (a decode step of a few tokens):
 // matrix-vector products on the CUDA cores, HBM-bound on the weights of the
 // experts hit.  A warp takes one output: the gate and up rows of a feature, or
-// one column of out over all of a token's slots, 16 bytes a lane and load.
+// one column of out over all of a token's slots, 16 bytes a lane and load.  Rows
+// of one expert read its weights again, which the rule for taking them counts.
 // One token through 8 of 256 experts of [768, 2048] (75 MB): the tile kernels
 // took 34 us on 48 and 64 of their 76 CTA pairs' tiles, without the copy and
 // the sum over slots that they need besides; these two take 23.
