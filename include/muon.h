@@ -492,7 +492,8 @@ muon_status_t muon_route_plan(const int32_t *idx, int64_t tokens, int32_t top_k,
 /* Gradient of the weights with respect to the logits (the choice is held
  * fixed): dlogits [tokens, experts] in the logits' dtype, row stride
  * dlogits_stride, from idx and dweights f32 [tokens, top_k].  Slots with
- * idx -1 (or out of range) contribute nothing. */
+ * idx -1 (or out of range) contribute nothing; the other slots of a token name
+ * different experts, as muon_route_forward's do. */
 muon_status_t muon_route_backward(const muon_route_config_t *cfg, const void *logits, int32_t dtype,
                                   int64_t stride, int64_t tokens, const int32_t *idx,
                                   const float *dweights, void *dlogits, int64_t dlogits_stride,
