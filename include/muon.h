@@ -330,11 +330,12 @@ int muon_debug_build(void);
  * that nothing satisfies, so that path can be tested without a GPU fault:
  *   what = 1  the next grouped-GEMM launch (matrices with min(M,N) > 64, or
  *             the allocation-free entry point): one CTA never arms one
- *             pipeline stage, and its MMA issuer's wait on it runs out; the
- *             same for the next product of muon_experts_backward, or of
- *             muon_experts_forward beyond a few (token, slot) pairs; or the next
- *             muon_rmsnorm_backward through a ring of bulk copies (many rows
- *             of 520 to 8192 columns): a row's copies are never issued;
+ *             pipeline stage, and its MMA issuer's wait on it runs out; or the
+ *             next product of muon_experts_backward, or of muon_experts_forward
+ *             beyond a few (token, slot) pairs: one CTA's MMA issuer waits for
+ *             what nothing provides; or the next muon_rmsnorm_backward through
+ *             a ring of bulk copies (many rows of 520 to 8192 columns): a row's
+ *             copies are never issued;
  *   what = 2  the next small-m launch (min(M,N) <= 64): the launch's last
  *             matrix is never published, and the waits for it run out;
  *   what = 0  cancels a pending request.

@@ -191,8 +191,8 @@ struct ExGemmParams {
   void* dw;
   int dw_dt, dw_vec;
   int stages;                     // ring depth (set at the launch)
-  int inject;                     // testing hook (set at the launch): CTA 0 arms its first
-                                  // stage and issues no copy for it
+  int inject;                     // testing hook (set at the launch): CTA 0's MMA issuer
+                                  // waits for what nothing provides
   int a_whole;                    // MN-major weights in one copy of two 64-column chunks
   unsigned* status;
   unsigned long long timeout_ns;

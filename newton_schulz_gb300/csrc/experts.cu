@@ -762,10 +762,6 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThread
           break;
         }
         if (crank == 0) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
-        if (p.inject && blockIdx.x == 0 && issued == 0) {      // testing hook: nothing comes for it
-          issued = stage = 1;
-          continue;
-        }
         const uint32_t bar = full0 + stage * 8;
         uint8_t* a = sStage + stage * kStageBytes;
         uint8_t* b = a + kOpBytes;
@@ -826,6 +822,10 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(kBoundThread
                                           : ptx::sdesc_kmajor_sw128(s0 + kOpBytes);
       const uint32_t a_lo = static_cast<uint32_t>(desc_a), b_lo = static_cast<uint32_t>(desc_b);
       const uint64_t a_hi = desc_a >> 32 << 32, b_hi = desc_b >> 32 << 32;
+      if (p.inject && blockIdx.x == 0) {      // testing hook: nothing arrives there before the end
+        if (lane == 0) stop = !wait_bounded(mma_drain, 0, abort_flag, p.status, p.timeout_ns, false);
+        stop = __shfl_sync(kFull, stop, 0);
+      }
       for (int tile = tile0, it = 0; tile < tiles && !stop; tile += tstep, ++it) {
         const Tile t = feed.get(p, scan, tiles, tile0, tstep, it, lane);
         if (t.kb == 0) continue;
@@ -998,6 +998,7 @@ template <int SLOTS>
 __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constant__ ExCombineParams p) {
   const int lane = threadIdx.x & 31;
   const int tokens = static_cast<int>(p.tokens), hidden = static_cast<int>(p.hidden);
+  const int yp = static_cast<int>(p.yp), yep = static_cast<int>(p.yep);
   // this lane's slot of a token: its row, -1 for none, and weight
   auto slot = [&](int64_t t, int32_t* row, float* w) {
     *row = -1;
@@ -1025,8 +1026,8 @@ __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
           const int64_t r = max(__shfl_sync(kFull, my_row, j0 + j), 0);
-          y[j] = *reinterpret_cast<const uint4*>(p.y + r * p.yp + cr);
-          e[j] = p.yexp[r * p.yep + (cr >> 5)];
+          y[j] = *reinterpret_cast<const uint4*>(p.y + r * yp + cr);
+          e[j] = p.yexp[r * yep + (cr >> 5)];
         }
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
