@@ -997,10 +997,11 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
 template <int SLOTS>
 __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constant__ ExCombineParams p) {
   const int lane = threadIdx.x & 31;
-  const int tokens = static_cast<int>(p.tokens), hidden = static_cast<int>(p.hidden);
+  const uint32_t tokens = static_cast<uint32_t>(p.tokens);      // below 2^31, as is its slots' number
+  const int hidden = static_cast<int>(p.hidden);
   const int yp = static_cast<int>(p.yp), yep = static_cast<int>(p.yep);
   // this lane's slot of a token: its row, -1 for none, and weight
-  auto slot = [&](int64_t t, int32_t* row, float* w) {
+  auto slot = [&](uint32_t t, int32_t* row, float* w) {
     *row = -1;
     *w = 1.f;
     if (t >= tokens || lane >= p.top_k) return;
@@ -1012,9 +1013,9 @@ __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constan
   float next_w;
   slot(blockIdx.x, &next_row, &next_w);
   ptx::wait_dependency();
-  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+  for (uint32_t t = blockIdx.x; t < tokens; t += gridDim.x) {
     const int32_t my_row = next_row < p.rows ? next_row : -1;
-    const float my_w = next_w;
+    const float my_w = my_row >= 0 ? next_w : 0.f;
     slot(t + gridDim.x, &next_row, &next_w);
     for (int c = threadIdx.x * 8; c - lane * 8 < hidden; c += blockDim.x * 8) {
       const int cr = min(c, static_cast<int>(p.yp) - 8);      // read column
@@ -1032,14 +1033,13 @@ __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
           const float wj = __shfl_sync(kFull, my_w, j0 + j);
-          const bool on = (live >> (j0 + j)) & 1u;
-          const float w = on ? wj * f((e[j] - 14u) << 23) : 0.f;
+          const float w = wj * f((max(e[j], kExpLeast) - 14u) << 23);
           const float2 w2 = make_float2(w, w);
-          const uint32_t keep = on ? ~0u : 0u;      // what row 0 holds may be anything
-          v[0] = ptx::fma2(w2, of_half(y[j].x & keep), v[0]);
-          v[1] = ptx::fma2(w2, of_half(y[j].y & keep), v[1]);
-          v[2] = ptx::fma2(w2, of_half(y[j].z & keep), v[2]);
-          v[3] = ptx::fma2(w2, of_half(y[j].w & keep), v[3]);
+          if (!((live >> (j0 + j)) & 1u)) y[j] = make_uint4(0u, 0u, 0u, 0u);
+          v[0] = ptx::fma2(w2, of_half(y[j].x), v[0]);
+          v[1] = ptx::fma2(w2, of_half(y[j].y), v[1]);
+          v[2] = ptx::fma2(w2, of_half(y[j].z), v[2]);
+          v[3] = ptx::fma2(w2, of_half(y[j].w), v[3]);
         }
       }
       const uint4 o = make_uint4(pack(v[0].x, v[0].y), pack(v[1].x, v[1].y), pack(v[2].x, v[2].y),
