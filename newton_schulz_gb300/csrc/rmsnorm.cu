@@ -15,8 +15,8 @@
 //
 // Of the measured copy rate: 16384 x 8192 bf16 with a residual 172 us, 0.92
 // (a ring of bulk copies 184 us); its gradient at 16384 x 4096 80 us, 0.98, and
-// 4 us for the gains' sums; 4099 x 2048 into e4m3 per 128 columns 19 us, 0.71:
-// the codes' conversions and two reductions a row show there.
+// 4 us for the gains' sums; 4099 x 2048 into e4m3 per 128 columns 19 us, 0.71: its
+// registers leave 25 warps an SM, too few for the loads' and conversions' latency.
 #include <cuda_fp8.h>
 
 #include <algorithm>

@@ -9,8 +9,9 @@
 // instruction issue: a token's 4 * experts bytes are little against its scores
 // and its top_k rounds.  16384 tokens over 256 experts in 8 groups, top 8: 19 us
 // (28.6 with expert e in lane e % 32, a reduction per group); the row plan of
-// its 131072 slots 9 us, its counts 2.5; the gradient of 16381 tokens over 128
-// experts 6 us.
+// its 131072 slots 9 us, its counts 2.5 (every block of the plan reads every tile's
+// counts: 57 us for 131072 tokens, 1865 for 2^20); the gradient of 16381 tokens
+// over 128 experts 6 us.
 #include <type_traits>
 
 #include "block.h"
