@@ -88,3 +88,22 @@ def test_training_calls():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, w.train(x, dout)))
+
+
+def test_gradient_through_clusters_and_copies_beside(monkeypatch):
+    # 16500 rows over 16 experts, K of 1024: the launch forms of a training batch
+    import sys
+    m = sys.modules[__name__]
+    monkeypatch.setattr(m, "HIDDEN", 1024)
+    monkeypatch.setattr(m, "INNER", 520)
+    w = Weights()
+    x, dout = _randn(16500, 1024, seed=7), _randn(16500, 1024, seed=8)
+    w.train(x, dout)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        got = w.train(x, dout)
+    x.copy_(_randn(16500, 1024, seed=9))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, w.train(x, dout)))
