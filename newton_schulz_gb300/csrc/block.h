@@ -37,9 +37,10 @@ void api_set_launches(int n);
 // Launch of a kernel that follows another of the same call.  early: it may
 // start while that one ends (programmatic dependent launch), and waits for its
 // results with ptx::wait_dependency before it touches what the call's kernels
-// share.  That saves 2 to 4 us a launch where the kernels are short (one token
-// through the experts' products 26.8 -> 21.3 us, 7 tokens' gradient in eight
-// launches 89 -> 52); under long ones the waiting blocks take room from the
+// share.  That saves 2 to 4 us a launch (one token through the experts' products
+// 26.8 -> 21.3 us, 7 tokens' gradient in eight launches 89 -> 52), also where the
+// kernels are long but their rows few (2 of 8 x [14336, 4096]: 34 rows 456 -> 446,
+// 4096 rows 951 -> 944); under many rows the waiting blocks take room from the
 // running ones (the products' gradient over 64 experts 1247 -> 1266 us).
 template <typename... A>
 cudaError_t launch_after(void (*kernel)(A...), dim3 grid, unsigned block, size_t smem, bool early,

@@ -569,7 +569,7 @@ bool few_rows(const muon_experts_t* a) {
   return (rows - hit) * 6.0 * static_cast<double>(a->hidden) * static_cast<double>(a->inner) <= 64e6;
 }
 
-constexpr int64_t kEarlyRows = 4096;  // most rows whose kernels are short: see launch_after
+constexpr int64_t kEarlyRows = 4096;  // most rows whose launches depend early: see launch_after
 constexpr int kSpreadBlocks = 5;      // per SM, for a copy that runs alone
 
 muon_status_t experts_impl(const muon_experts_t* a, void* out, int64_t outs, void* gu, cudaStream_t stream) {

@@ -411,14 +411,14 @@ __device__ __forceinline__ void epi_up(const ExGemmParams& p, const Tile& t, con
 // Rows for the sum over slots, as 16-bit floats (IEEE half) with one exponent
 // per row and 32 features (a warp's lanes): q = v * 2^(14 - e), e the exponent of
 // the piece's largest finite value; infinities and NaN stay what and where they
-// are.  A value keeps 11 bits while it is above 2^-28 of
-// that largest one (below, its error is 2^-39 of it): a term errs by at most 2^-11
-// of itself, an eighth of what the bf16 operand behind it and the bf16 result
-// add, whatever its neighbours hold.  (15-bit integers, uniform in a piece, gave a
-// feature beside one 1000 times larger an error of 2.6 %; bf16 rows would add as
-// much as the result's rounding.)  Half of fp32's bytes are written and read
-// (16384 tokens over 256 x [768, 2048], product and sum: 398 + 167 us with fp32
-// rows, 378 + 91 with 16 bits).
+// are.  A value keeps 11 bits while it is above 2^-28 of that largest one (below,
+// its error is 2^-39 of it): a term errs by at most 2^-11 of itself, an eighth of
+// what the bf16 operand behind it and the bf16 result add, whatever its neighbours
+// hold.  (15-bit integers, uniform in a piece, gave a feature beside one 1000
+// times larger an error of 2.6 %; bf16 rows would add as much as the result's
+// rounding.)  Half of fp32's bytes are written and read (16384 tokens over 256 x
+// [768, 2048], product and sum: 398 + 167 us with fp32 rows, 378 + 91 with 16 bits
+// when they were compared; 327 + 93 now).
 __device__ __forceinline__ void epi_rows(const ExGemmParams& p, const Tile& t, const EpiWarp& w) {
   const int orow = w.tid >> 4, chunk = w.tid & 15, h = w.m0 + chunk * 8;
   __half* const y = p.y + static_cast<int64_t>(t.urow + orow) * p.yp + h;
@@ -993,7 +993,7 @@ __global__ void __launch_bounds__(256, 5) ex_spread_kernel(const __grid_constant
 // out[t] = sum over slots, in slot order, a block per token, eight columns a
 // lane, SLOTS slots' loads in flight and the next token's rows with them;
 // HBM-bound once the conversions are few (no branch per slot: a slot without a row
-// reads row 0 and takes zeros): 16384 tokens of 8 slots of 2048 in 92 us, 6.3 TB/s.
+// reads row 0 and takes zeros): 16384 tokens of 8 slots of 2048 in 93 us, 6.3 TB/s.
 template <int SLOTS>
 __global__ void __launch_bounds__(256, 3) ex_combine_kernel(const __grid_constant__ ExCombineParams p) {
   const int lane = threadIdx.x & 31;
